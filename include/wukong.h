@@ -75,7 +75,8 @@ typedef enum {
                               the output is not valid */
 } wk_status;
 
-typedef enum { WK_F32 = 0, WK_BF16 = 1, WK_F16 = 2 } wk_dtype;
+typedef enum { WK_F32 = 0, WK_BF16 = 1, WK_F16 = 2,
+               WK_E4M3 = 3 /* 8-bit rows of a cache (wk_cache) */ } wk_dtype;
 
 /* Shape of the stack; every layer has the same shape (n is the same for every
  * layer because n_F + n_L = n). Scaling knobs of section 2.3: num_layers = l,
@@ -488,6 +489,127 @@ WK_API wk_status wk_whale_attention(const void* Hw, const void* Hs, void* A, int
 WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_whale_weights* w, void* Hf,
                                      int64_t rows, int32_t d, int32_t h, wk_dtype dtype, float eps,
                                      wk_stream_t stream);
+
+/* ---- attention over behaviour sequences: jagged batches, gradients, a paged cache ----
+ *
+ * The WHALE pages (section 2.1 item 3) let the interaction rows of an example attend over that
+ * user's behaviour sequence, and scale the sequences to 15k events (section 2.2). wk_whale_attention
+ * above is the module's own form: one head, K = V, every sequence of one length. The calls below are
+ * the general form: separate keys and values, several heads with shared key heads, sequences of
+ * different lengths (none at all among them), the gradients, and histories that are kept from
+ * request to request in a paged cache, in 16 bits or quantised to 8.
+ *
+ * Jagged tensors. The sequences of a batch lie one after another in [tokens, heads, d] tensors;
+ * offsets (int32, batch + 1 of them, on the device, not decreasing) hold their boundaries. Query
+ * head h reads key head h / (q_heads / kv_heads). With row i of sequence b and its keys j:
+ *
+ *   S[i, j] = scale * <Q[i], K[j]>,  P = softmax over j,  O[i] = sum_j P[i, j] V[j]
+ *
+ * and lse[i] = log sum_j exp S[i, j]. A row that sees no key has O = 0 and lse = -inf, and its
+ * gradients are 0. Rows of tensors behind the last boundary are neither read into a result nor
+ * written, whatever they hold; neither are rows of one sequence into the result of another.
+ *
+ * Offsets, lengths and page tables are on the device, so their content is checked there: where they
+ * point outside the tensors, or a sequence is longer than max_q / max_kv says, the access is
+ * left out, the result is not valid, and wk_device_status returns WK_ERR_DEVICE.
+ *
+ * Arithmetic: 16-bit inputs and outputs; products accumulate in fp32; scores, softmax statistics
+ * and lse are fp32; the softmax weights and the gradients of the scores are rounded to the 16-bit
+ * type as tensor-core operands. Results do not depend on the order in which blocks run. */
+
+typedef struct {
+  int32_t batch;               /* sequences, >= 0 */
+  int32_t q_heads, kv_heads;   /* q_heads a multiple of kv_heads */
+  int32_t d;                   /* head width: 32, 64, 128 or 160 */
+  int32_t max_q, max_kv;       /* most query rows / most keys of one sequence */
+  int64_t total_q, total_kv;   /* rows of Q and O / of K and V (total_kv: not read by the cache calls) */
+  int64_t q_stride, k_stride, v_stride; /* elements from one token to the next of Q, K, V; 0: heads * d.
+                                  Multiples of 8. Heads of a token are d apart. Every other tensor is dense */
+  wk_dtype dtype;              /* WK_BF16 or WK_F16: Q, K, V, O and the gradients */
+  float scale;                 /* 0 selects 1 / sqrt(d) */
+} wk_xattn_config;
+
+/* Bytes of device workspace that wk_xattn_forward (backward == 0) or wk_xattn_backward
+ * (backward != 0) needs for this configuration; 0 if none. The workspace is the caller's: calls
+ * that may run at the same time (other streams, graphs replayed side by side) need one each. It
+ * need not be initialised and carries nothing from call to call. Needs no device. Errors:
+ * WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED as wk_xattn_forward. */
+WK_API wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* bytes);
+
+/* O [total_q, q_heads, d] and, unless NULL, lse [total_q, q_heads] fp32 of Q [total_q, q_heads, d]
+ * over K, V [total_kv, kv_heads, d]. q_off, kv_off: batch + 1 offsets. kv_lens: batch lengths, of
+ * sequence b's rows the first kv_lens[b] are keys (padded batches: kv_off[b] = b * L), or NULL:
+ * all are. V may be K (shared keys and values). O must not overlap Q, K or V. Pointers 16-byte
+ * aligned, the offsets 4-byte. Asynchronous on `stream`; may be captured. Errors:
+ * WK_ERR_INVALID_ARG (NULL, misaligned, negative or inconsistent sizes, workspace too small,
+ * O overlapping an input), WK_ERR_UNSUPPORTED (d, dtype, a stride that is no multiple of 8),
+ * WK_ERR_CUDA. */
+WK_API wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V,
+                                  const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_lens, void* O,
+                                  float* lse, void* workspace, int64_t workspace_bytes, wk_stream_t stream);
+
+/* Gradients of sum(O * dO): dQ [total_q, q_heads, d], dK and dV [total_kv, kv_heads, d], dense, in
+ * cfg->dtype, overwritten. O and lse are those of the forward of the same inputs. The gradients of
+ * a key head are summed over the query heads that share it. Rows between a sequence's kv_lens[b]
+ * and the next boundary get zeros. With V = K the gradient of the shared tensor is dK + dV.
+ * Deterministic: two calls on the same inputs give the same bits. Errors as wk_xattn_forward. */
+WK_API wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V,
+                                   const void* O, const float* lse, const void* dO, const int32_t* q_off,
+                                   const int32_t* kv_off, const int32_t* kv_lens, void* dQ, void* dK, void* dV,
+                                   void* workspace, int64_t workspace_bytes, wk_stream_t stream);
+
+/* A paged cache of keys and values. Position p of a sequence is row p % page_size of the page that
+ * entry p / page_size of the sequence's row of a page table names. Pages may be shared by sequences
+ * that only read them.
+ *   K, V          [num_pages, kv_heads, page_size, d] of dtype
+ *   K_exp, V_exp  [num_pages, kv_heads, page_size] uint8, with WK_E4M3 only (else NULL)
+ * With WK_E4M3 a row (one token, one head) is held as e4m3 values times a power of two of its own:
+ * x = value * 2^(exp - 127), where 2^(exp - 127) is the least power of two, from 2^-127 on, with
+ * max |x| <= 448 * 2^(exp - 127), and values are rounded to nearest, ties to even. Scaling by a
+ * power of two is exact, so the one rounding is e4m3's own. A row that holds inf or NaN has
+ * exp = 255 and reads back as NaN. */
+typedef struct {
+  void *K, *V;
+  uint8_t *K_exp, *V_exp;
+  int32_t num_pages, page_size; /* page_size 16, 32, 64 or 128 */
+  int32_t kv_heads, d;          /* d 32, 64, 128 or 160 */
+  wk_dtype dtype;               /* WK_BF16, WK_F16 or WK_E4M3 */
+} wk_cache;
+
+/* Writes new tokens into the cache: K, V [total_new, kv_heads, d] (dtype, strides as
+ * wk_xattn_config) hold, for sequence b, the tokens new_off[b] .. new_off[b + 1], which are the
+ * LAST ones of its kv_lens[b] positions (kv_lens counts them). table [batch, table_width] int32.
+ * A 16-bit cache takes tokens of its own type. Two tokens must not go to one place (a page that two
+ * sequences append to): what that row then holds is one of the two, or a mix. Entries of the table
+ * that no new token needs are not read. Errors: WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED (d,
+ * page_size, dtypes), WK_ERR_CUDA. */
+WK_API wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, int64_t k_stride,
+                                int64_t v_stride, wk_dtype dtype, const int32_t* new_off, const int32_t* table,
+                                int32_t table_width, const int32_t* kv_lens, int32_t batch, int64_t total_new,
+                                int32_t max_new, wk_stream_t stream);
+
+/* Reads cached sequences back: position p < kv_lens[b] of sequence b into row out_off[b] + p of K, V
+ * [total, kv_heads, d] (dense, 16-bit; of a 16-bit cache its own type), rounded to `dtype` from the
+ * value held. Only rows below out_off[b + 1] are written; those past kv_lens[b] stay as they were.
+ * Errors as wk_cache_write. */
+WK_API wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t table_width,
+                               const int32_t* kv_lens, const int32_t* out_off, void* K, void* V, wk_dtype dtype,
+                               int32_t batch, int64_t total, int32_t max_kv, wk_stream_t stream);
+
+/* Bytes of workspace of wk_cache_attention, as wk_xattn_workspace. */
+WK_API wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xattn_config* cfg, int64_t* bytes);
+
+/* Attention of each sequence's query rows q_off[b] .. q_off[b + 1] over its kv_lens[b] cached keys:
+ * one new token per sequence, a chunk of them, or a prompt. causal != 0: the rows are the newest
+ * tokens, row i of n sees the keys at positions <= kv_lens[b] - n + i (its own, already written,
+ * among them); causal == 0: every row sees every key (candidates over a history). cfg->kv_heads and
+ * cfg->d are the cache's; cfg->dtype is the type of Q and O (a 16-bit cache's own). Keys and values
+ * of an 8-bit cache enter with the values they stand for. table, kv_lens as wk_cache_write; O, lse,
+ * workspace, errors as wk_xattn_forward. */
+WK_API wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, const void* Q,
+                                    const int32_t* q_off, const int32_t* table, int32_t table_width,
+                                    const int32_t* kv_lens, int causal, void* O, float* lse, void* workspace,
+                                    int64_t workspace_bytes, wk_stream_t stream);
 
 /* ---- one layer without allocating: for callers that cannot call cudaMalloc ----
  *

@@ -370,3 +370,74 @@ def layer_backward(cfg, w, X, dOut, ln_eps=1e-5):
     dP = np.einsum("eic,jc->eij", dF, c["Y"])
     dX += np.einsum("eij,ejt->eit", dP + dP.transpose(0, 2, 1), c["X"])
     return dX, g
+
+
+# ------------------------------------------------ attention over behaviour sequences
+
+def sequence_attention(Q, K, V, scale=None, new_rows=None):
+    """(O, lse) in float64 of one sequence: Q [n, hq, d], K, V [L, hk, d], query head h reading key
+    head h // (hq // hk). new_rows=n: the rows are the newest n of the L positions, row i sees keys up
+    to L - n + i. A row that sees no key: O = 0, lse = -inf."""
+    Q, K, V = _c64(Q), _c64(K), _c64(V)
+    n, hq, d = Q.shape
+    L, hk, _ = K.shape
+    scale = 1.0 / np.sqrt(d) if not scale else scale
+    O = np.zeros((n, hq, d))
+    lse = np.full((n, hq), -np.inf)
+    for h in range(hq):
+        for i in range(n):
+            seen = L if new_rows is None else max(0, min(L, L - new_rows + i + 1))
+            if seen == 0:
+                continue
+            s = (K[:seen, h // (hq // hk)] @ Q[i, h]) * scale
+            m = s.max()
+            e = np.exp(s - m)
+            lse[i, h] = m + np.log(e.sum())
+            O[i, h] = (e / e.sum()) @ V[:seen, h // (hq // hk)]
+    return O, lse
+
+
+def sequence_attention_backward(Q, K, V, dO, scale=None):
+    """(dQ, dK, dV) of sum(O * dO) in float64; shapes as sequence_attention."""
+    Q, K, V, dO = _c64(Q), _c64(K), _c64(V), _c64(dO)
+    hq, d = Q.shape[1:]
+    hk = K.shape[1]
+    scale = 1.0 / np.sqrt(d) if not scale else scale
+    dQ, dK, dV = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+    if K.shape[0] == 0:
+        return dQ, dK, dV
+    for h in range(hq):
+        g = h // (hq // hk)
+        S = Q[:, h] @ K[:, g].T * scale
+        P = np.exp(S - S.max(axis=1, keepdims=True))
+        P /= P.sum(axis=1, keepdims=True)
+        dP = dO[:, h] @ V[:, g].T
+        dS = P * (dP - (dP * P).sum(axis=1, keepdims=True)) * scale
+        dQ[:, h] = dS @ K[:, g]
+        dK[:, g] += dS.T @ Q[:, h]
+        dV[:, g] += P.T @ dO[:, h]
+    return dQ, dK, dV
+
+
+def e4m3_round(x):
+    """float64 values of magnitude <= 448 rounded to e4m3 (nearest, ties to even): 3 fraction bits from 2^-6 up,
+    steps of 2^-9 below."""
+    x = _c64(x)
+    _, p = np.frexp(np.maximum(np.abs(x), 2.0 ** -6))  # |x| = f * 2^p with f in [1/2, 1)
+    step = np.ldexp(1.0, p - 4)
+    return np.round(x / step) * step
+
+
+def cache_quantise(rows):
+    """(values, exponents) of rows [..., d]: x ~ value * 2^(exponent - 127), the least power of two from 2^-127 on
+    with max |x| <= 448 * 2^(exponent - 127); exponent 255 (and values NaN) for a row with inf or NaN."""
+    rows = _c64(rows)
+    amax = np.abs(rows).max(axis=-1)
+    e = np.zeros(amax.shape, dtype=np.int64)
+    for t in range(255):
+        e = np.where(amax > 448.0 * 2.0 ** (t - 127), t + 1, e)
+    bad = ~np.isfinite(rows).all(axis=-1)
+    e = np.where(bad, 255, e)
+    with np.errstate(invalid="ignore"):
+        v = e4m3_round(np.where(bad[..., None], 0.0, rows) * np.ldexp(1.0, 127 - np.where(bad, 127, e))[..., None])
+    return np.where(bad[..., None], np.nan, v), e.astype(np.uint8)

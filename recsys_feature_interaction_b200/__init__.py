@@ -19,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libwukong.so")
 
 WK_OK, WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED, WK_ERR_OOM, WK_ERR_CUDA, WK_ERR_TIMEOUT, WK_ERR_DEVICE, WK_ERR_NONFINITE = range(8)
-WK_F32, WK_BF16, WK_F16 = 0, 1, 2
+WK_F32, WK_BF16, WK_F16, WK_E4M3 = 0, 1, 2, 3
 (WK_KERNEL_FM_LN, WK_KERNEL_MLP_GEMM, WK_KERNEL_LCB, WK_KERNEL_RES_LN, WK_KERNEL_CONVERT, WK_KERNEL_MOE_GATE,
  WK_KERNEL_MOE_COMBINE, WK_KERNEL_HEAD, WK_KERNEL_WHALE_ATTN, WK_KERNEL_WHALE_FFN, WK_KERNEL_BW_CONTRACT,
  WK_KERNEL_BW_ROWS, WK_KERNEL_FRONT, WK_KERNEL_COUNT) = range(14)
@@ -70,6 +70,20 @@ class WkWhaleWeights(ctypes.Structure):
                 ("ln_beta", ctypes.c_void_p), ("W_up", ctypes.c_void_p), ("W_down", ctypes.c_void_p)]
 
 
+class WkXattnConfig(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("total_q", ctypes.c_int64), ("total_kv", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class WkCache(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_exp", ctypes.c_void_p),
+                ("V_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -117,6 +131,15 @@ def lib():
             "wk_whale_kernel_times": [vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)],
             "wk_whale_attention": [vp, vp, vp, i64, i32, i32, i32, ci, vp],
             "wk_whale_fusion_ffn": [vp, vp, ctypes.POINTER(WkWhaleWeights), vp, i64, i32, i32, ci, cf, vp],
+            "wk_xattn_workspace": [ctypes.POINTER(WkXattnConfig), ci, ctypes.POINTER(i64)],
+            "wk_xattn_forward": [ctypes.POINTER(WkXattnConfig)] + [vp] * 9 + [i64, vp],
+            "wk_xattn_backward": [ctypes.POINTER(WkXattnConfig)] + [vp] * 13 + [i64, vp],
+            "wk_cache_write": [ctypes.POINTER(WkCache), vp, vp, i64, i64, ci, vp, vp, i32, vp, i32, i64, i32, vp],
+            "wk_cache_read": [ctypes.POINTER(WkCache), vp, i32, vp, vp, vp, vp, ci, i32, i64, i32, vp],
+            "wk_cache_attention_workspace": [ctypes.POINTER(WkCache), ctypes.POINTER(WkXattnConfig),
+                                             ctypes.POINTER(i64)],
+            "wk_cache_attention": [ctypes.POINTER(WkCache), ctypes.POINTER(WkXattnConfig), vp, vp, vp, i32, vp, ci,
+                                   vp, vp, vp, i64, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -586,3 +609,179 @@ def wk_whale_fusion_ffn(Hw, A, weights, Hf, rows, d, h, dtype, eps=0.0, stream=N
     ww = _whale_weights(weights)
     _check(lib().wk_whale_fusion_ffn(_addr(Hw), _addr(A), ctypes.byref(ww), _addr(Hf), int(rows), int(d), int(h),
                                      _dtype_code(dtype), float(eps), _stream(stream, Hw)), "wk_whale_fusion_ffn")
+
+
+# ------------------------------------- attention over behaviour sequences, paged cache
+
+def _int32(t, name, *shape):
+    """Device int32 data of the given leading sizes (None: any), dense; its address."""
+    if t is None:
+        return None
+    if str(t.dtype) != "torch.int32" or t.dim() != len(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d dimensions" % (name, len(shape)))
+    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    return t.data_ptr()
+
+
+def _tokens(t, name):
+    """(rows, heads, d, elements from token to token) of a [tokens, heads, d] tensor whose heads are dense."""
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, d]" % name)
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError("the heads of a token of %s must be dense" % name)
+    return n, h, d, (t.stride(0) if n > 1 else h * d)
+
+
+def _dense(t, name, shape, dtype):
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+    return t.data_ptr()
+
+
+def _call(name, args, stream, tensors):
+    """Calls lib().<name>(*args, stream) with the tensors' device as the current one."""
+    import torch
+
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1 or next(iter(devs)).type != "cuda":
+        raise ValueError("%s takes tensors of one CUDA device, got %s" % (name, sorted(map(str, devs))))
+    with torch.cuda.device(next(iter(devs))):
+        _check(getattr(lib(), name)(*args, _stream(stream, tensors[0])), name)
+
+
+def _scratch(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return (workspace.data_ptr() if workspace.numel() else None), workspace.numel() * workspace.element_size()
+
+
+def _xattn_config(Q, K, V, batch, max_q, max_kv, scale):
+    tq, hq, d, qs = _tokens(Q, "Q")
+    tk, hk, dk, ks = _tokens(K, "K")
+    tv, hv, dv, vs = _tokens(V, "V")
+    if dk != d or dv != d or hv != hk or tv != tk or K.dtype != Q.dtype or V.dtype != Q.dtype:
+        raise ValueError("Q, K and V disagree: %s, %s, %s" % (tuple(Q.shape), tuple(K.shape), tuple(V.shape)))
+    return WkXattnConfig(int(batch), hq, hk, d, int(max_q), int(max_kv), tq, tk, qs, ks, vs, _dtype_code(Q.dtype),
+                         float(scale))
+
+
+def wk_xattn_workspace(Q, K, batch, max_q, max_kv, backward=False):
+    """Bytes of device workspace that the forward (or the backward) of these tensors needs."""
+    c = _xattn_config(Q, K, K, batch, max_q, max_kv, 0.0)
+    n = ctypes.c_int64()
+    _check(lib().wk_xattn_workspace(ctypes.byref(c), int(bool(backward)), ctypes.byref(n)), "wk_xattn_workspace")
+    return n.value
+
+
+def wk_xattn_forward(Q, K, V, O, q_off, kv_off, max_q, max_kv, kv_lens=None, lse=None, scale=0.0, workspace=None,
+                     stream=None):
+    """O[i] = softmax(scale * Q[i] K^T) V of jagged sequences: Q, O [tokens, q_heads, d], K, V [tokens, kv_heads, d]
+    (tokens may be strided), q_off, kv_off int32 boundaries [batch + 1], kv_lens int32 [batch] or None, lse fp32
+    [tokens, q_heads] or None. workspace: a tensor of at least wk_xattn_workspace bytes, this call's own while it runs."""
+    import torch
+
+    batch = q_off.shape[0] - 1
+    c = _xattn_config(Q, K, V, batch, max_q, max_kv, scale)
+    args = [ctypes.byref(c), _addr(Q), _addr(K), _addr(V), _int32(q_off, "q_off", None),
+            _int32(kv_off, "kv_off", batch + 1), _int32(kv_lens, "kv_lens", batch), _dense(O, "O", Q.shape, Q.dtype),
+            _dense(lse, "lse", Q.shape[:2], torch.float32), *_scratch(workspace)]
+    _call("wk_xattn_forward", args, stream, [Q, K, V, O, q_off, kv_off, kv_lens, lse, workspace])
+
+
+def wk_xattn_backward(Q, K, V, O, lse, dO, dQ, dK, dV, q_off, kv_off, max_q, max_kv, kv_lens=None, scale=0.0,
+                      workspace=None, stream=None):
+    """Gradients of sum(O * dO) for the forward of the same arguments: dQ, dK, dV (dense) are overwritten."""
+    import torch
+
+    batch = q_off.shape[0] - 1
+    c = _xattn_config(Q, K, V, batch, max_q, max_kv, scale)
+    args = [ctypes.byref(c), _addr(Q), _addr(K), _addr(V), _dense(O, "O", Q.shape, Q.dtype),
+            _dense(lse, "lse", Q.shape[:2], torch.float32), _dense(dO, "dO", Q.shape, Q.dtype),
+            _int32(q_off, "q_off", None), _int32(kv_off, "kv_off", batch + 1), _int32(kv_lens, "kv_lens", batch),
+            _dense(dQ, "dQ", Q.shape, Q.dtype), _dense(dK, "dK", K.shape, Q.dtype), _dense(dV, "dV", V.shape, Q.dtype),
+            *_scratch(workspace)]
+    _call("wk_xattn_backward", args, stream, [Q, K, V, O, lse, dO, dQ, dK, dV, q_off, kv_off, kv_lens, workspace])
+
+
+def _cache(cache):
+    """cache: mapping with K, V [pages, kv_heads, page_size, d] (16-bit, or 8-bit: float8_e4m3fn or uint8) and, with
+    8 bits, K_exp, V_exp uint8 [pages, kv_heads, page_size]."""
+    K, V, ke, ve = cache["K"], cache["V"], cache.get("K_exp"), cache.get("V_exp")
+    if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or not K.is_contiguous() or not V.is_contiguous():
+        raise ValueError("a cache's K and V must be contiguous [pages, kv_heads, page_size, d] tensors of one type")
+    eight = K.element_size() == 1
+    if eight and str(K.dtype) not in ("torch.float8_e4m3fn", "torch.uint8"):
+        raise ValueError("an 8-bit cache holds e4m3 values")
+    for t in (ke, ve):
+        if eight != (t is not None):
+            raise ValueError("K_exp and V_exp belong to 8-bit caches, and to those only")
+        if t is not None and (t.shape != K.shape[:3] or str(t.dtype) != "torch.uint8" or not t.is_contiguous()):
+            raise ValueError("K_exp and V_exp must be contiguous uint8 [pages, kv_heads, page_size]")
+    return WkCache(_addr(K), _addr(V), _addr(ke), _addr(ve), K.shape[0], K.shape[2], K.shape[1], K.shape[3],
+                   WK_E4M3 if eight else _dtype_code(K.dtype)), [K, V, ke, ve]
+
+
+def wk_cache_write(cache, K, V, new_off, table, kv_lens, max_new, stream=None):
+    """Writes the newest tokens of each sequence, rows new_off[b]..new_off[b + 1] of K, V [tokens, kv_heads, d], to
+    their places in the paged cache (quantised with 8-bit caches). kv_lens counts them; table [batch, width] int32."""
+    c, held = _cache(cache)
+    n, h, d, ks = _tokens(K, "K")
+    nv, hv, dv, vs = _tokens(V, "V")
+    if (n, h, d) != (nv, hv, dv) or (h, d) != (c.kv_heads, c.d) or V.dtype != K.dtype:
+        raise ValueError("K, V and the cache disagree")
+    batch = new_off.shape[0] - 1
+    args = [ctypes.byref(c), _addr(K), _addr(V), ks, vs, _dtype_code(K.dtype), _int32(new_off, "new_off", None),
+            _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch), batch, n,
+            int(max_new)]
+    _call("wk_cache_write", args, stream, [K, V, new_off, table, kv_lens] + held)
+
+
+def wk_cache_read(cache, table, kv_lens, out_off, K, V, max_kv, stream=None):
+    """Reads the cached sequences into rows out_off[b] .. out_off[b] + kv_lens[b] of K, V [tokens, kv_heads, d]."""
+    c, held = _cache(cache)
+    batch = out_off.shape[0] - 1
+    if K.dim() != 3 or tuple(K.shape[1:]) != (c.kv_heads, c.d):
+        raise ValueError("K must be [tokens, kv_heads, d] of the cache")
+    args = [ctypes.byref(c), _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
+            _int32(out_off, "out_off", None), _dense(K, "K", K.shape, K.dtype), _dense(V, "V", K.shape, K.dtype),
+            _dtype_code(K.dtype), batch, K.shape[0], int(max_kv)]
+    _call("wk_cache_read", args, stream, [K, V, out_off, table, kv_lens] + held)
+
+
+def _cache_config(c, Q, batch, max_q, max_kv, scale):
+    tq, hq, d, qs = _tokens(Q, "Q")
+    return WkXattnConfig(int(batch), hq, c.kv_heads, d, int(max_q), int(max_kv), tq, 0, qs, 0, 0, _dtype_code(Q.dtype),
+                         float(scale))
+
+
+def wk_cache_attention_workspace(cache, Q, batch, max_q, max_kv):
+    """Bytes of device workspace that wk_cache_attention needs."""
+    c, _ = _cache(cache)
+    cfg = _cache_config(c, Q, batch, max_q, max_kv, 0.0)
+    n = ctypes.c_int64()
+    _check(lib().wk_cache_attention_workspace(ctypes.byref(c), ctypes.byref(cfg), ctypes.byref(n)),
+           "wk_cache_attention_workspace")
+    return n.value
+
+
+def wk_cache_attention(cache, Q, O, q_off, table, kv_lens, max_q, max_kv, causal=True, lse=None, scale=0.0,
+                       workspace=None, stream=None):
+    """Attention of each sequence's rows of Q (its newest tokens when causal, candidates otherwise) over its cached
+    keys. Q, O [tokens, q_heads, d]; table [batch, width], kv_lens [batch], q_off [batch + 1] int32."""
+    import torch
+
+    c, held = _cache(cache)
+    batch = q_off.shape[0] - 1
+    cfg = _cache_config(c, Q, batch, max_q, max_kv, scale)
+    ws, nws = _scratch(workspace)
+    args = [ctypes.byref(c), ctypes.byref(cfg), _addr(Q), _int32(q_off, "q_off", None),
+            _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
+            int(bool(causal)), _dense(O, "O", Q.shape, Q.dtype), _dense(lse, "lse", Q.shape[:2], torch.float32),
+            *_scratch(workspace)]
+    _call("wk_cache_attention", args, stream, [Q, O, q_off, table, kv_lens, lse, workspace] + held)

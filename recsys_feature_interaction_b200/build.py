@@ -12,16 +12,31 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "_lib", "libwukong.so")
-SOURCES = ["wk_api.cu"]
-HEADERS = ["common.cuh", "gemm_tc.cuh", "gemm_tc2.cuh", "lcb_tc.cuh", "fm_tc.cuh", "front_tc.cuh", "res_ln.cuh", "res_ln_ring.cuh", "simt.cuh", "convert.cuh", "moe.cuh", "head.cuh", "whale.cuh", "backward.cuh", "bw_tc.cuh"]
+COMMON = ["common.cuh", "host.cuh"]
+# each source and the headers it is compiled from
+SOURCES = {
+    "wk_api.cu": COMMON + ["gemm_tc.cuh", "gemm_tc2.cuh", "lcb_tc.cuh", "fm_tc.cuh", "front_tc.cuh", "res_ln.cuh",
+                           "res_ln_ring.cuh", "simt.cuh", "convert.cuh", "moe.cuh", "head.cuh", "whale.cuh",
+                           "backward.cuh", "bw_tc.cuh"],
+    "wk_seq.cu": COMMON + ["seq_index.h", "seq.cuh"],
+}
+
+
+def _object(source):
+    return os.path.join(HERE, "_lib", source.replace(".cu", ".o"))
+
+
+def _older(target, source):
+    """Whether `target` is missing or older than the source, its headers or the public header."""
+    if not os.path.exists(target):
+        return True
+    t = os.path.getmtime(target)
+    deps = [os.path.join(CSRC, f) for f in [source] + SOURCES[source]] + [os.path.join(INCLUDE, "wukong.h")]
+    return any(os.path.getmtime(p) > t for p in deps)
 
 
 def _stale():
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "wukong.h")]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return any(_older(LIB, s) for s in SOURCES)
 
 
 def nvcc_flags():
@@ -31,17 +46,32 @@ def nvcc_flags():
 
 
 def build(force=False, verbose=False):
+    """Compiles the sources that changed side by side, one object each, and links them."""
     if not force and not _stale():
         return LIB
-    os.makedirs(os.path.dirname(LIB), exist_ok=True)
-    cmd = ["nvcc", "-shared"] + nvcc_flags() + ["-o", LIB] + [os.path.join(CSRC, s) for s in SOURCES]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    libdir = os.path.dirname(LIB)
+    os.makedirs(libdir, exist_ok=True)
+    running = []
+    for s in SOURCES:
+        if force or _older(_object(s), s):
+            with open(_object(s) + ".log", "w") as log:
+                cmd = ["nvcc", "-c"] + nvcc_flags() + ["-o", _object(s), os.path.join(CSRC, s)]
+                running.append((s, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)))
+    failed = [s for s, p in running if p.wait() != 0]
+    logs = "".join(open(_object(s) + ".log").read() for s in (failed or SOURCES))
+    if failed:
+        for s in failed:
+            if os.path.exists(_object(s)):
+                os.remove(_object(s))
+        raise RuntimeError("nvcc failed:\n" + logs)
+    r = subprocess.run(["nvcc", "-shared"] + nvcc_flags() + ["-o", LIB] + [_object(s) for s in SOURCES],
+                       capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
-    with open(os.path.join(os.path.dirname(LIB), "ptxas.log"), "w") as f:
-        f.write(r.stdout + r.stderr)
+    with open(os.path.join(libdir, "ptxas.log"), "w") as f:
+        f.write(logs)
     if verbose:
-        print(r.stdout + r.stderr)
+        print(logs)
     return LIB
 
 

@@ -13,8 +13,6 @@
 // bf16 on request) and fp32 accumulation; every intermediate buffer holds T. A
 // bf16 stack's weights are converted to T once, at create, and its input once per
 // forward. The stack output is written in the caller's type.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -28,6 +26,7 @@
 
 #include "wukong.h"
 #include "common.cuh"
+#include "host.cuh"
 #include "convert.cuh"
 #include "fm_tc.cuh"
 #include "front_tc.cuh"
@@ -52,19 +51,13 @@ __device__ unsigned g_standalone_status;
 typedef __nv_bfloat16 bf16;
 typedef __half f16;
 
-// ------------------------------------------------------------ device context
-
-struct DevInfo {
-  bool init = false;
-  int id = 0;
-  int sms = 0;
-  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  unsigned* standalone_status = nullptr;
-};
-
 std::mutex g_mu;
 DevInfo g_dev[64];
 std::set<std::pair<int, const void*>> g_smem_attr;
+
+}  // namespace
+
+namespace wk {
 
 wk_status dev_info(DevInfo** out) {
   int dev = 0;
@@ -112,27 +105,15 @@ wk_status smem_attr(const DevInfo* dv, const void* fn, int bytes) {
   return WK_OK;
 }
 
-inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace wk
 
-inline wk_status launch_status() {
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? WK_OK : WK_ERR_CUDA;
-}
+namespace {
 
 inline size_t dtype_bytes(wk_dtype t) { return t == WK_F32 ? 4 : 2; }
 
-template <typename T>
-constexpr CUtensorMapDataType tmap_dtype() {
-  return sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                        : (Half16<T>::kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
-}
-template <>
-constexpr CUtensorMapDataType tmap_dtype<float>() {
-  return CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-}
+}  // namespace
 
-// Tiled tensor map; dims[0] is the contiguous dimension, strides in bytes for dims 1..rank-1.
-bool make_map(const DevInfo* dv, CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const void* base,
+bool wk::make_map(const DevInfo* dv, CUtensorMap* m, CUtensorMapDataType dt, uint32_t rank, const void* base,
               const uint64_t* dims, const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
   cuuint64_t gd[5];
   cuuint64_t gs[4];
@@ -148,6 +129,8 @@ bool make_map(const DevInfo* dv, CUtensorMap* m, CUtensorMapDataType dt, uint32_
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // --------------------------------------------------------------- GEMM maps
 

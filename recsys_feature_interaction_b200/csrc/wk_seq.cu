@@ -1,0 +1,371 @@
+// wk_seq.cu -- the C ABI of attention over behaviour sequences (include/wukong.h): argument
+// checks, workspaces and launches of the jagged cross attention, its gradients and the paged cache.
+// The kernels are in seq.cuh.
+#include <algorithm>
+#include <cmath>
+
+#include "wukong.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "seq.cuh"
+
+using namespace wk;
+
+namespace {
+
+typedef __nv_bfloat16 bf16;
+typedef __half f16;
+
+bool seq_d_ok(int d) { return d == 32 || d == 64 || d == 128 || d == 160; }
+bool type16(wk_dtype t) { return t == WK_BF16 || t == WK_F16; }
+bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The largest number of rows a tensor may have: byte offsets stay far inside 64 bits.
+constexpr int64_t kMaxRows = int64_t{1} << 40;
+
+// Stride in elements from token to token: 0 means dense.
+int64_t stride_of(int64_t s, int heads, int d) { return s == 0 ? static_cast<int64_t>(heads) * d : s; }
+
+// Bytes from the first to the last element of [rows, heads, d] with a token stride.
+int64_t extent(int64_t rows, int64_t stride, int heads, int d) {
+  return rows <= 0 ? 0 : ((rows - 1) * stride + static_cast<int64_t>(heads) * d) * 2;
+}
+
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uint8_t *x = static_cast<const uint8_t*>(a), *y = static_cast<const uint8_t*>(b);
+  return an > 0 && bn > 0 && x && y && x < y + bn && y < x + an;
+}
+
+wk_status check_config(const wk_xattn_config* c) {
+  if (!c || c->batch < 0 || c->q_heads < 1 || c->kv_heads < 1 || c->q_heads % c->kv_heads != 0 || c->max_q < 0 ||
+      c->max_kv < 0 || c->total_q < 0 || c->total_kv < 0 || c->total_q > kMaxRows || c->total_kv > kMaxRows ||
+      !(c->scale >= 0.f) || !std::isfinite(c->scale))
+    return WK_ERR_INVALID_ARG;
+  if (!seq_d_ok(c->d) || !type16(c->dtype) || c->q_heads > 1024) return WK_ERR_UNSUPPORTED;
+  const int64_t qs = stride_of(c->q_stride, c->q_heads, c->d), ks = stride_of(c->k_stride, c->kv_heads, c->d),
+                vs = stride_of(c->v_stride, c->kv_heads, c->d);
+  const int64_t qd = static_cast<int64_t>(c->q_heads) * c->d, kd = static_cast<int64_t>(c->kv_heads) * c->d;
+  if (qs < qd || ks < kd || vs < kd || qs > (1 << 30) || ks > (1 << 30) || vs > (1 << 30)) return WK_ERR_INVALID_ARG;
+  if (qs % 8 != 0 || ks % 8 != 0 || vs % 8 != 0) return WK_ERR_UNSUPPORTED;
+  return WK_OK;
+}
+
+wk_status check_cache(const wk_cache* c) {
+  if (!c || c->num_pages < 0 || c->kv_heads < 1) return WK_ERR_INVALID_ARG;
+  if (!seq_d_ok(c->d) || c->kv_heads > 1024 ||
+      (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) ||
+      (!type16(c->dtype) && c->dtype != WK_E4M3))
+    return WK_ERR_UNSUPPORTED;
+  if (c->num_pages > 0 && (!c->K || !c->V || !al16(c->K) || !al16(c->V))) return WK_ERR_INVALID_ARG;
+  const bool q8 = c->dtype == WK_E4M3;
+  if (c->num_pages > 0 && q8 && (!c->K_exp || !c->V_exp || !al16(c->K_exp) || !al16(c->V_exp)))
+    return WK_ERR_INVALID_ARG;
+  if (!q8 && (c->K_exp || c->V_exp)) return WK_ERR_INVALID_ARG;
+  return WK_OK;
+}
+
+int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+SeqArgs make_args(const wk_xattn_config& c, const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_lens,
+                  unsigned* status) {
+  SeqArgs a{};
+  a.batch = c.batch;
+  a.q_heads = c.q_heads;
+  a.kv_heads = c.kv_heads;
+  a.max_q = c.max_q;
+  a.max_kv = c.max_kv;
+  a.total_q = c.total_q;
+  a.total_kv = c.total_kv;
+  a.q_stride = stride_of(c.q_stride, c.q_heads, c.d);
+  a.k_stride = stride_of(c.k_stride, c.kv_heads, c.d);
+  a.v_stride = stride_of(c.v_stride, c.kv_heads, c.d);
+  a.scale = c.scale > 0.f ? c.scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.d)));
+  a.q_off = q_off;
+  a.kv_off = kv_off;
+  a.kv_lens = kv_lens;
+  a.status = status;
+  return a;
+}
+
+void cache_args(SeqArgs* a, const wk_cache& c, const int32_t* table, int32_t width) {
+  a->table = table;
+  a->table_width = width;
+  a->num_pages = c.num_pages;
+  a->page_shift = shift_of(c.page_size);
+  a->kv_heads = c.kv_heads;
+  a->k_exp = c.K_exp;
+  a->v_exp = c.V_exp;
+}
+
+constexpr int kWarps = 8;
+bool grid_of(int64_t warps, unsigned* grid) {
+  const int64_t g = (warps + kWarps - 1) / kWarps;
+  if (g > INT32_MAX) return false;
+  *grid = static_cast<unsigned>(g);
+  return true;
+}
+
+// Calls f with the head width and the 16-bit type as compile-time values.
+template <typename F>
+wk_status with_type(int d, wk_dtype t, F f) {
+  const bool b = t == WK_BF16;
+  switch (d) {
+    case 32: return b ? f.template operator()<32, bf16>() : f.template operator()<32, f16>();
+    case 64: return b ? f.template operator()<64, bf16>() : f.template operator()<64, f16>();
+    case 128: return b ? f.template operator()<128, bf16>() : f.template operator()<128, f16>();
+    case 160: return b ? f.template operator()<160, bf16>() : f.template operator()<160, f16>();
+  }
+  return WK_ERR_UNSUPPORTED;
+}
+
+struct RunForward {
+  const void *Q, *K, *V;
+  void* O;
+  float* lse;
+  SeqArgs a;
+  int src;
+  cudaStream_t st;
+  template <int D, typename T, int SRC>
+  wk_status run() const {
+    unsigned grid;
+    if (!grid_of(static_cast<int64_t>(a.batch) * a.max_q * a.q_heads, &grid)) return WK_ERR_UNSUPPORTED;
+    xattn_forward_kernel<D, T, SRC><<<grid, 32 * kWarps, 0, st>>>(static_cast<const T*>(Q), K, V, static_cast<T*>(O),
+                                                                  lse, a);
+    return launch_status();
+  }
+  template <int D, typename T>
+  wk_status operator()() const {
+    return src == 0 ? run<D, T, 0>() : src == 1 ? run<D, T, 1>() : run<D, T, 2>();
+  }
+};
+
+struct RunBackward {
+  const void *Q, *K, *V, *O, *dO;
+  const float* lse;
+  void *dQ, *dK, *dV;
+  float* delta;
+  SeqArgs a;
+  cudaStream_t st;
+  template <int D, typename T>
+  wk_status operator()() const {
+    unsigned g0, g1, g2;
+    const int64_t rows = a.total_q * a.q_heads;
+    if (!grid_of(rows, &g0) || !grid_of(static_cast<int64_t>(a.batch) * a.max_q * a.q_heads, &g1) ||
+        !grid_of(a.total_kv * a.kv_heads, &g2))
+      return WK_ERR_UNSUPPORTED;
+    const T *q = static_cast<const T*>(Q), *k = static_cast<const T*>(K), *v = static_cast<const T*>(V),
+            *go = static_cast<const T*>(dO);
+    if (g0) xattn_delta_kernel<D, T><<<g0, 32 * kWarps, 0, st>>>(static_cast<const T*>(O), go, delta, rows);
+    if (g1) xattn_dq_kernel<D, T><<<g1, 32 * kWarps, 0, st>>>(q, k, v, go, lse, delta, static_cast<T*>(dQ), a);
+    if (g2)
+      xattn_dkv_kernel<D, T>
+          <<<g2, 32 * kWarps, 0, st>>>(q, k, v, go, lse, delta, static_cast<T*>(dK), static_cast<T*>(dV), a);
+    return launch_status();
+  }
+};
+
+struct RunWrite {
+  const wk_cache& c;
+  const void *K, *V;
+  SeqArgs a;
+  unsigned grid;
+  cudaStream_t st;
+  template <int D, typename T>
+  wk_status operator()() const {
+    const T *k = static_cast<const T*>(K), *v = static_cast<const T*>(V);
+    if (c.dtype == WK_E4M3)
+      cache_write_kernel<D, T, true><<<grid, 32 * kWarps, 0, st>>>(k, v, c.K, c.V, c.K_exp, c.V_exp, a);
+    else
+      cache_write_kernel<D, T, false><<<grid, 32 * kWarps, 0, st>>>(k, v, c.K, c.V, nullptr, nullptr, a);
+    return launch_status();
+  }
+};
+
+struct RunRead {
+  const wk_cache& c;
+  void *K, *V;
+  SeqArgs a;
+  unsigned grid;
+  cudaStream_t st;
+  template <int D, typename T>
+  wk_status operator()() const {
+    T *k = static_cast<T*>(K), *v = static_cast<T*>(V);
+    if (c.dtype == WK_E4M3) cache_read_kernel<D, T, 2><<<grid, 32 * kWarps, 0, st>>>(c.K, c.V, k, v, a);
+    else cache_read_kernel<D, T, 1><<<grid, 32 * kWarps, 0, st>>>(c.K, c.V, k, v, a);
+    return launch_status();
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* bytes) {
+  if (!bytes) return WK_ERR_INVALID_ARG;
+  const wk_status s = check_config(cfg);
+  if (s != WK_OK) return s;
+  *bytes = backward ? cfg->total_q * cfg->q_heads * 4 : 0;
+  return WK_OK;
+}
+
+wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V,
+                           const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_lens, void* O, float* lse,
+                           void* workspace, int64_t workspace_bytes, wk_stream_t stream) {
+  wk_status s = check_config(cfg);
+  if (s != WK_OK) return s;
+  if (cfg->batch == 0 || cfg->total_q == 0 || cfg->max_q == 0) return WK_OK;
+  const bool keys = cfg->total_kv > 0;
+  if (!Q || !O || !q_off || !kv_off || (keys && (!K || !V)) || !al16(Q) || !al16(K) || !al16(V) || !al16(O) ||
+      !al4(q_off) || !al4(kv_off) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
+    return WK_ERR_INVALID_ARG;
+  int64_t need = 0;
+  s = wk_xattn_workspace(cfg, 0, &need);
+  if (s != WK_OK) return s;
+  if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;
+  SeqArgs a = make_args(*cfg, q_off, kv_off, kv_lens, nullptr);
+  const int64_t ob = extent(cfg->total_q, static_cast<int64_t>(cfg->q_heads) * cfg->d, cfg->q_heads, cfg->d);
+  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)) ||
+      overlap(O, ob, K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)) ||
+      overlap(O, ob, V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)))
+    return WK_ERR_INVALID_ARG;
+  DevInfo* dv = nullptr;
+  s = dev_info(&dv);
+  if (s != WK_OK) return s;
+  a.status = dv->standalone_status;
+  return with_type(cfg->d, cfg->dtype, RunForward{Q, K, V, O, lse, a, 0, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V, const void* O,
+                            const float* lse, const void* dO, const int32_t* q_off, const int32_t* kv_off,
+                            const int32_t* kv_lens, void* dQ, void* dK, void* dV, void* workspace,
+                            int64_t workspace_bytes, wk_stream_t stream) {
+  wk_status s = check_config(cfg);
+  if (s != WK_OK) return s;
+  if (cfg->batch == 0) return WK_OK;
+  const bool keys = cfg->total_kv > 0, rows = cfg->total_q > 0;
+  if (!q_off || !kv_off || (rows && (!Q || !O || !lse || !dO || !dQ)) || (keys && (!K || !V || !dK || !dV)) ||
+      !al16(Q) || !al16(K) || !al16(V) || !al16(O) || !al16(dO) || !al16(dQ) || !al16(dK) || !al16(dV) ||
+      !al4(q_off) || !al4(kv_off) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
+    return WK_ERR_INVALID_ARG;
+  int64_t need = 0;
+  s = wk_xattn_workspace(cfg, 1, &need);
+  if (s != WK_OK) return s;
+  if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;
+  SeqArgs a = make_args(*cfg, q_off, kv_off, kv_lens, nullptr);
+  // no gradient may lie over an input or another gradient
+  const int64_t qd = static_cast<int64_t>(cfg->q_heads) * cfg->d, kd = static_cast<int64_t>(cfg->kv_heads) * cfg->d;
+  const int64_t qb = cfg->total_q * qd * 2, kb = cfg->total_kv * kd * 2;
+  const struct {
+    const void* p;
+    int64_t n;
+  } in[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
+            {K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)},
+            {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)},
+            {O, qb}, {dO, qb}, {lse, cfg->total_q * cfg->q_heads * 4}, {workspace, need}},
+    out[] = {{dQ, qb}, {dK, kb}, {dV, kb}};
+  for (int i = 0; i < 3; ++i) {
+    for (const auto& x : in)
+      if (overlap(out[i].p, out[i].n, x.p, x.n)) return WK_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return WK_ERR_INVALID_ARG;
+  }
+  if (!rows && !keys) return WK_OK;
+  DevInfo* dv = nullptr;
+  s = dev_info(&dv);
+  if (s != WK_OK) return s;
+  a.status = dv->standalone_status;
+  return with_type(cfg->d, cfg->dtype,
+                   RunBackward{Q, K, V, O, dO, lse, dQ, dK, dV, static_cast<float*>(workspace), a,
+                               reinterpret_cast<cudaStream_t>(stream)});
+}
+
+wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, int64_t k_stride, int64_t v_stride,
+                         wk_dtype dtype, const int32_t* new_off, const int32_t* table, int32_t table_width,
+                         const int32_t* kv_lens, int32_t batch, int64_t total_new, int32_t max_new,
+                         wk_stream_t stream) {
+  wk_status s = check_cache(cache);
+  if (s != WK_OK) return s;
+  if (batch < 0 || total_new < 0 || total_new > kMaxRows || max_new < 0 || table_width < 0) return WK_ERR_INVALID_ARG;
+  if (!type16(dtype) || (cache->dtype != WK_E4M3 && cache->dtype != dtype)) return WK_ERR_UNSUPPORTED;
+  wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, max_new, 0, total_new, total_new, 0, k_stride,
+                      v_stride, dtype, 0.f};
+  s = check_config(&cfg);
+  if (s != WK_OK) return s;
+  if (batch == 0 || total_new == 0 || max_new == 0) return WK_OK;
+  if (!K || !V || !new_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
+      !al4(new_off) || !al4(table) || !al4(kv_lens))
+    return WK_ERR_INVALID_ARG;
+  SeqArgs a = make_args(cfg, new_off, nullptr, kv_lens, nullptr);
+  cache_args(&a, *cache, table, table_width);
+  unsigned grid;
+  if (!grid_of(static_cast<int64_t>(batch) * max_new * cache->kv_heads * 2, &grid)) return WK_ERR_UNSUPPORTED;
+  DevInfo* dv = nullptr;
+  s = dev_info(&dv);
+  if (s != WK_OK) return s;
+  a.status = dv->standalone_status;
+  return with_type(cache->d, dtype, RunWrite{*cache, K, V, a, grid, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t table_width, const int32_t* kv_lens,
+                        const int32_t* out_off, void* K, void* V, wk_dtype dtype, int32_t batch, int64_t total,
+                        int32_t max_kv, wk_stream_t stream) {
+  wk_status s = check_cache(cache);
+  if (s != WK_OK) return s;
+  if (batch < 0 || total < 0 || total > kMaxRows || max_kv < 0 || table_width < 0) return WK_ERR_INVALID_ARG;
+  if (!type16(dtype) || (cache->dtype != WK_E4M3 && cache->dtype != dtype)) return WK_ERR_UNSUPPORTED;
+  if (batch == 0 || total == 0 || max_kv == 0) return WK_OK;
+  if (!K || !V || !out_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
+      !al4(out_off) || !al4(table) || !al4(kv_lens))
+    return WK_ERR_INVALID_ARG;
+  const int64_t bytes = total * cache->kv_heads * cache->d * 2;
+  if (overlap(K, bytes, V, bytes)) return WK_ERR_INVALID_ARG;
+  wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
+  SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
+  cache_args(&a, *cache, table, table_width);
+  unsigned grid;
+  if (!grid_of(static_cast<int64_t>(batch) * max_kv * cache->kv_heads * 2, &grid)) return WK_ERR_UNSUPPORTED;
+  DevInfo* dv = nullptr;
+  s = dev_info(&dv);
+  if (s != WK_OK) return s;
+  a.status = dv->standalone_status;
+  return with_type(cache->d, dtype, RunRead{*cache, K, V, a, grid, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xattn_config* cfg, int64_t* bytes) {
+  if (!bytes) return WK_ERR_INVALID_ARG;
+  wk_status s = check_cache(cache);
+  if (s != WK_OK) return s;
+  s = check_config(cfg);
+  if (s != WK_OK) return s;
+  if (cfg->kv_heads != cache->kv_heads || cfg->d != cache->d) return WK_ERR_INVALID_ARG;
+  if (cache->dtype != WK_E4M3 && cache->dtype != cfg->dtype) return WK_ERR_UNSUPPORTED;
+  *bytes = 0;
+  return WK_OK;
+}
+
+wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, const void* Q, const int32_t* q_off,
+                             const int32_t* table, int32_t table_width, const int32_t* kv_lens, int causal, void* O,
+                             float* lse, void* workspace, int64_t workspace_bytes, wk_stream_t stream) {
+  int64_t need = 0;
+  wk_status s = wk_cache_attention_workspace(cache, cfg, &need);
+  if (s != WK_OK) return s;
+  if (table_width < 0) return WK_ERR_INVALID_ARG;
+  if (cfg->batch == 0 || cfg->total_q == 0 || cfg->max_q == 0) return WK_OK;
+  if (!Q || !O || !q_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(Q) || !al16(O) ||
+      !al4(q_off) || !al4(table) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
+    return WK_ERR_INVALID_ARG;
+  if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;
+  SeqArgs a = make_args(*cfg, q_off, nullptr, kv_lens, nullptr);
+  cache_args(&a, *cache, table, table_width);
+  a.causal = causal != 0;
+  const int64_t ob = cfg->total_q * cfg->q_heads * cfg->d * 2;
+  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d))) return WK_ERR_INVALID_ARG;
+  DevInfo* dv = nullptr;
+  s = dev_info(&dv);
+  if (s != WK_OK) return s;
+  a.status = dv->standalone_status;
+  return with_type(cfg->d, cfg->dtype, RunForward{Q, cache->K, cache->V, O, lse, a, cache->dtype == WK_E4M3 ? 2 : 1,
+                                                  reinterpret_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"
