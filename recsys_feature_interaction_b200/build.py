@@ -6,6 +6,7 @@ uses the caller's CUDA context when there is one.
 """
 import os
 import subprocess
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,7 +19,7 @@ SOURCES = {
     "wk_api.cu": COMMON + ["gemm_tc.cuh", "gemm_tc2.cuh", "lcb_tc.cuh", "fm_tc.cuh", "front_tc.cuh", "res_ln.cuh",
                            "res_ln_ring.cuh", "simt.cuh", "convert.cuh", "moe.cuh", "head.cuh", "whale.cuh",
                            "backward.cuh", "bw_tc.cuh"],
-    "wk_seq.cu": COMMON + ["seq_index.h", "seq.cuh"],
+    "wk_seq.cu": COMMON + ["seq_index.h", "seq_args.cuh", "seq.cuh", "seq_cache.cuh", "seq_rows.cuh"],
 }
 
 
@@ -76,5 +77,5 @@ def build(force=False, verbose=False):
 
 
 if __name__ == "__main__":
-    build(force=True)
+    build(force="force" in sys.argv[1:])
     print(LIB)

@@ -5,92 +5,13 @@
 
 #include <cuda_fp8.h>
 
-#include "common.cuh"
-#include "seq_index.h"
+#include "seq_args.cuh"
 
 namespace wk {
-
-struct SeqArgs {
-  int32_t batch, q_heads, kv_heads, max_q, max_kv;
-  int64_t total_q, total_kv;
-  int64_t q_stride, k_stride, v_stride;
-  float scale;
-  const int32_t *q_off, *kv_off, *kv_lens;
-  // cache
-  const int32_t* table;
-  int32_t table_width, num_pages, page_shift, causal;
-  const uint8_t *k_exp, *v_exp;
-  unsigned* status;
-};
-
-// 2^(e - 127) of a cache row's exponent byte; NaN for 255.
-__device__ __forceinline__ float seq_pow(uint8_t e) {
-  return __uint_as_float(e == 255 ? 0x7FC00000u : (e == 0 ? 0x00400000u : static_cast<uint32_t>(e) << 23));
-}
 
 __device__ __forceinline__ float seq_e4m3(uint8_t v) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(v, __NV_E4M3);
   return __half2float(__half(h));
-}
-
-// ---------------------------------------------------------------- cache write
-
-// One warp per (new token, kv head, K or V).
-template <int D, typename T, bool Q8>
-__global__ void cache_write_kernel(const T* __restrict__ K, const T* __restrict__ V, void* cK, void* cV, uint8_t* eK,
-                                   uint8_t* eV, SeqArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t per_seq = static_cast<int64_t>(a.max_q) * a.kv_heads * 2;
-  const int64_t b = unit / per_seq;
-  if (b >= a.batch) return;
-  const int r = static_cast<int>(unit % per_seq);
-  const int i = r / (a.kv_heads * 2), h = (r >> 1) % a.kv_heads, which = r & 1;
-  const SeqSpan q = seq_span(a.q_off, nullptr, b, a.total_q, a.max_q);
-  const SeqSpan kv = seq_cached(a.kv_lens, b, static_cast<int64_t>(a.table_width) << a.page_shift, INT32_MAX);
-  if (q.bad || kv.bad || kv.len < q.len) {
-    if (lane == 0) flag_error(a.status, kFlagBadShape);
-    return;
-  }
-  if (i >= q.len) return;
-  const int64_t pos = static_cast<int64_t>(kv.len) - q.len + i;
-  const int page = seq_page(a.table + b * a.table_width, pos, a.page_shift, a.num_pages);
-  if (page < 0) {
-    if (lane == 0) flag_error(a.status, kFlagBadShape);
-    return;
-  }
-  const int64_t row = ((static_cast<int64_t>(page) * a.kv_heads + h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-  const T* src = (which ? V + (q.begin + i) * a.v_stride : K + (q.begin + i) * a.k_stride) + h * D;
-  float x[D / 32], amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) x[c] = Half16<T>::to(src[c * 32 + lane]);
-  if constexpr (Q8) {
-    bool odd = false;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      amax = fmaxf(amax, fabsf(x[c]));
-      odd |= !(fabsf(x[c]) < INFINITY);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-    odd = __any_sync(~0u, odd);
-    int e = 0;  // biased
-    if (!odd && amax > 0.f) {
-      int p;
-      const float f = frexpf(amax, &p);
-      e = min(max(p - 9 + (f > 0.875f ? 1 : 0) + 127, 0), 254);
-    }
-    uint8_t* dst = static_cast<uint8_t*>(which ? cV : cK) + row * D;
-    const double inv = odd ? 0. : ldexp(1., 127 - e);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-      dst[c * 32 + lane] = __nv_cvt_float_to_fp8(static_cast<float>(x[c] * inv), __NV_SATFINITE, __NV_E4M3);
-    if (lane == 0) (which ? eV : eK)[row] = odd ? 255 : e;
-  } else {
-    T* dst = static_cast<T*>(which ? cV : cK) + row * D;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = src[c * 32 + lane];
-  }
 }
 
 // ---------------------------------------------------------------- key rows
@@ -134,35 +55,6 @@ template <int D, typename T, int SRC>
 __device__ __forceinline__ SeqRows<D, T, SRC> seq_rows(const SeqArgs& a, const void* base, const uint8_t* ex,
                                                        int64_t stride, int64_t b, int64_t begin, int h) {
   return {base, ex, stride, begin, SRC ? a.table + b * a.table_width : nullptr, h};
-}
-
-template <int SRC>
-__device__ __forceinline__ SeqSpan seq_keys(const SeqArgs& a, int64_t b) {
-  if constexpr (SRC == 0) return seq_span(a.kv_off, a.kv_lens, b, a.total_kv, a.max_kv);
-  return seq_cached(a.kv_lens, b, static_cast<int64_t>(a.table_width) << a.page_shift, a.max_kv);
-}
-
-// ---------------------------------------------------------------- cache read
-
-template <int D, typename T, int SRC>
-__global__ void cache_read_kernel(const void* cK, const void* cV, T* __restrict__ K, T* __restrict__ V, SeqArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t per_seq = static_cast<int64_t>(a.max_kv) * a.kv_heads * 2;
-  const int64_t b = unit / per_seq;
-  if (b >= a.batch) return;
-  const int64_t r = unit % per_seq;
-  const int j = static_cast<int>(r / (a.kv_heads * 2)), h = static_cast<int>((r >> 1) % a.kv_heads), which = r & 1;
-  const SeqSpan kv = seq_keys<SRC>(a, b);
-  const SeqSpan out = seq_span(a.kv_off, nullptr, b, a.total_kv, INT32_MAX);
-  if (kv.bad || out.bad || out.room < kv.len)
-    if (lane == 0) flag_error(a.status, kFlagBadShape);
-  if (j >= kv.len || j >= out.room) return;
-  float x[D / 32];
-  if (!seq_rows<D, T, SRC>(a, which ? cV : cK, which ? a.v_exp : a.k_exp, 0, b, 0, h).load(a, j, lane, x)) return;
-  T* dst = (which ? V : K) + ((out.begin + j) * a.kv_heads + h) * D;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) dst[c * 32 + lane] = Half16<T>::from(x[c]);
 }
 
 // ---------------------------------------------------------------- forward

@@ -1,0 +1,284 @@
+// seq_args.cuh -- what every sequence kernel is given, and how the work of a jagged batch is shared
+// out among the blocks of a grid.
+//
+// Units. A unit is R packed query rows of one (sequence, key head): row r of a sequence is query
+// row r / group of query head h * group + r % group, so that the query heads that share a key head
+// share its loads. Unit (b, h, t) costs max(1, key blocks its last row sees); the units of a batch,
+// in the order (b, h, t), make one line of key blocks. The line is cut into equal pieces, one per
+// thread block: no block has more than ceil(T / grid) key blocks to do, however ragged the batch and
+// however few its rows, and which block does what depends on the lengths alone. A unit that a cut
+// goes through is finished by the combine kernel from fp32 partial results: piece c leaves those of
+// the unit it enters in the middle in slot 2c, those of the unit it leaves unfinished in slot 2c + 1.
+#pragma once
+
+#include "common.cuh"
+#include "seq_index.h"
+
+namespace wk {
+
+struct SeqArgs {
+  int32_t batch, q_heads, kv_heads, max_q, max_kv;
+  int64_t total_q, total_kv;
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  const int32_t *q_off, *kv_off, *kv_lens;
+  // cache
+  const int32_t* table;
+  int32_t table_width, num_pages, page_shift, causal;
+  const uint8_t *k_exp, *v_exp;
+  unsigned* status;
+};
+
+// Where key rows come from: jagged tensors, a 16-bit cache, an 8-bit cache.
+enum { SEQ_JAGGED = 0, SEQ_PAGED16 = 1, SEQ_PAGED8 = 2 };
+
+template <int SRC>
+__device__ __forceinline__ SeqSpan seq_keys(const SeqArgs& a, int64_t b) {
+  if constexpr (SRC == SEQ_JAGGED) return seq_span(a.kv_off, a.kv_lens, b, a.total_kv, a.max_kv);
+  return seq_cached(a.kv_lens, b, static_cast<int64_t>(a.table_width) << a.page_shift, a.max_kv);
+}
+
+__device__ __forceinline__ SeqSpan seq_queries(const SeqArgs& a, int64_t b) {
+  return seq_span(a.q_off, nullptr, b, a.total_q, a.max_q);
+}
+
+// 2^(e - 127) of a cache row's exponent byte; NaN for 255.
+__device__ __forceinline__ float seq_pow(uint32_t e) {
+  return __uint_as_float(e == 255 ? 0x7FC00000u : (e == 0 ? 0x00400000u : e << 23));
+}
+
+// 2^x (the hardware's approximate base-2 exponential; 2^-inf = +0).
+__device__ __forceinline__ float seq_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One (sequence, key head, row tile) and the key blocks [j0, j1) of it that a piece holds.
+struct SeqUnit {
+  int32_t b, h, t;
+  int32_t j0, j1, nb;   // nb: the unit's cost (1 for a unit without keys)
+  int32_t n, rows;      // query rows of the sequence; packed rows n * group
+  int32_t len;          // keys of the sequence
+  int64_t q_begin, kv_begin;
+};
+
+// Cost of row tile t of a sequence.
+template <int R, int KB>
+__device__ __forceinline__ int seq_tile_cost(const SeqArgs& a, int n, int len, int group, int t) {
+  const int last = (min((t + 1) * R, n * group) - 1) / group;
+  const int nb = (seq_seen(len, n, last, a.causal) + KB - 1) / KB;
+  return nb > 1 ? nb : 1;
+}
+
+template <int R, int KB, int SRC>
+__device__ __forceinline__ int64_t seq_cost(const SeqArgs& a, int64_t b) {
+  const SeqSpan q = seq_queries(a, b), kv = seq_keys<SRC>(a, b);
+  const int group = a.q_heads / a.kv_heads;
+  const int tiles = (q.len * group + R - 1) / R;
+  int64_t s = 0;
+  if (a.causal) {
+    for (int t = 0; t < tiles; ++t) s += seq_tile_cost<R, KB>(a, q.len, kv.len, group, t);
+  } else if (tiles) {
+    s = static_cast<int64_t>(tiles) * seq_tile_cost<R, KB>(a, q.len, kv.len, group, 0);
+  }
+  return s * a.kv_heads;
+}
+
+// What the threads of a block find out together at its start: how long the line is, how much of it
+// one piece is, and the place on it that this block begins at.
+struct SeqPlace {
+  int64_t per, begin, end;  // key blocks per piece; this piece's part of the line
+  int32_t b;                // sequence that holds `begin`
+  int64_t into;             // key blocks from that sequence's start to `begin`
+};
+
+// All threads call it (it synchronises the block); sh: NT / 32 + 4 values of shared memory. With
+// `tell`, spans out of range set the status word (block 0 only: it sees every sequence).
+template <int R, int KB, int SRC, int NT>
+__device__ SeqPlace seq_place(const SeqArgs& a, int64_t piece, int64_t pieces, int64_t* sh, bool tell) {
+  const int tid = threadIdx.x;
+  const int64_t each = (a.batch + NT - 1) / NT;
+  const int64_t b0 = min(static_cast<int64_t>(a.batch), tid * each), b1 = min(static_cast<int64_t>(a.batch), b0 + each);
+  int64_t sum = 0;
+  for (int64_t b = b0; b < b1; ++b) {
+    sum += seq_cost<R, KB, SRC>(a, b);
+    if (tell && (seq_queries(a, b).bad || seq_keys<SRC>(a, b).bad)) flag_error(a.status, kFlagBadShape);
+  }
+  // inclusive scan over the block
+  const int lane = tid & 31, warp = tid >> 5;
+  int64_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh[warp] = x;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += sh[w];
+    total += sh[w];
+  }
+  x += before;
+  SeqPlace p;
+  p.per = (total + pieces - 1) / pieces;
+  if (p.per < 1) p.per = 1;
+  p.begin = min(piece * p.per, total);
+  p.end = min(p.begin + p.per, total);
+  p.b = a.batch;
+  p.into = 0;
+  if (x - sum <= p.begin && p.begin < x) {  // exactly one thread's sequences hold it
+    int64_t at = x - sum;
+    for (int64_t b = b0; b < b1; ++b) {
+      const int64_t c = seq_cost<R, KB, SRC>(a, b);
+      if (p.begin < at + c) {
+        sh[NT / 32] = b;
+        sh[NT / 32 + 1] = p.begin - at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+  if (p.begin < p.end) {
+    p.b = static_cast<int32_t>(sh[NT / 32]);
+    p.into = sh[NT / 32 + 1];
+  }
+  __syncthreads();
+  return p;
+}
+
+// Walks the units of a piece.
+template <int R, int KB, int SRC>
+struct SeqWalk {
+  int64_t left;  // key blocks of the piece still to do
+  SeqUnit u;
+  int32_t tiles, group;
+
+  // Reads sequence u.b (or the next one that has rows); false behind the last.
+  __device__ __forceinline__ bool open(const SeqArgs& a) {
+    for (; u.b < a.batch; ++u.b) {
+      const SeqSpan q = seq_queries(a, u.b);
+      if (q.len == 0) continue;
+      const SeqSpan kv = seq_keys<SRC>(a, u.b);
+      u.n = q.len;
+      u.rows = q.len * group;
+      u.q_begin = q.begin;
+      u.kv_begin = kv.begin;
+      u.len = kv.len;
+      tiles = (u.rows + R - 1) / R;
+      u.h = u.t = 0;
+      return true;
+    }
+    return false;
+  }
+
+  // Puts the walk at the piece's first unit; u.j0 is then where the piece enters it.
+  __device__ __forceinline__ void start(const SeqArgs& a, const SeqPlace& p) {
+    group = a.q_heads / a.kv_heads;
+    left = p.end - p.begin;
+    if (left <= 0) return;
+    u.b = p.b;
+    open(a);
+    int64_t into = p.into;
+    if (!a.causal) {  // every tile of the sequence costs the same
+      const int64_t c = seq_tile_cost<R, KB>(a, u.n, u.len, group, 0);
+      const int64_t skip = into / c;
+      u.h = static_cast<int32_t>(skip / tiles);
+      u.t = static_cast<int32_t>(skip % tiles);
+      into -= skip * c;
+    } else {
+      for (;;) {
+        const int64_t c = seq_tile_cost<R, KB>(a, u.n, u.len, group, u.t);
+        if (into < c) break;
+        into -= c;
+        if (++u.t == tiles) {
+          u.t = 0;
+          ++u.h;
+        }
+      }
+    }
+    u.j0 = static_cast<int32_t>(into);
+  }
+
+  // The next unit of the piece in u; false at its end. Call start() first.
+  __device__ __forceinline__ bool next(const SeqArgs& a) {
+    if (left <= 0) return false;
+    u.nb = seq_tile_cost<R, KB>(a, u.n, u.len, group, u.t);
+    u.j1 = static_cast<int32_t>(min(static_cast<int64_t>(u.nb), u.j0 + left));
+    left -= u.j1 - u.j0;
+    return true;
+  }
+  // Moves past the unit that next() gave.
+  __device__ __forceinline__ void advance(const SeqArgs& a) {
+    u.j0 = 0;
+    if (left <= 0) return;
+    if (++u.t == tiles) {
+      u.t = 0;
+      if (++u.h == a.kv_heads) {
+        ++u.b;
+        open(a);
+      }
+    }
+  }
+};
+
+// fp32 partial results of a piece of a unit: O [R, D] not normalised, then m [R] (base 2), l [R].
+template <int R, int D>
+struct SeqSlot {
+  static constexpr int64_t kFloats = static_cast<int64_t>(R) * (D + 2);
+  static __device__ __forceinline__ float* at(float* ws, int64_t slot) { return ws + slot * kFloats; }
+};
+
+__device__ __forceinline__ int64_t seq_slot_of(int64_t piece, bool enters) { return 2 * piece + (enters ? 0 : 1); }
+
+// Combines the pieces of cut units: block c does the unit that the cut before piece c goes through,
+// if that is the unit's first cut. m and l of a row that a piece saw no key of are -inf and 0.
+constexpr int SEQ_COMBINE_THREADS = 256;
+template <int R, int KB, int D, int SRC, typename T>
+__global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
+    seq_combine_kernel(float* ws, T* __restrict__ O, float* __restrict__ lse, SeqArgs a, int64_t pieces) {
+  __shared__ int64_t sh[SEQ_COMBINE_THREADS / 32 + 4];
+  const int64_t c = blockIdx.x + 1;
+  const SeqPlace p = seq_place<R, KB, SRC, SEQ_COMBINE_THREADS>(a, c, pieces, sh, false);
+  if (p.begin >= p.end) return;
+  SeqWalk<R, KB, SRC> w;
+  w.start(a, p);
+  if (w.u.j0 == 0) return;                       // the cut lies between two units
+  const int64_t f0 = p.begin - w.u.j0;           // the unit's place on the line
+  if (f0 / p.per != c - 1) return;               // an earlier cut is its first
+  const int nb = seq_tile_cost<R, KB>(a, w.u.n, w.u.len, w.group, w.u.t);
+  const int64_t last = (f0 + nb - 1) / p.per;
+  const int r0 = w.u.t * R, rows = min(R, w.u.rows - r0);
+#if __CUDA_ARCH__ >= 900
+  cudaGridDependencySynchronize();
+#endif
+  for (int i = threadIdx.x; i < rows * (D / 4); i += SEQ_COMBINE_THREADS) {
+    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    float m = -INFINITY;
+    for (int64_t k = c - 1; k <= last; ++k)
+      m = fmaxf(m, SeqSlot<R, D>::at(ws, seq_slot_of(k, k != c - 1))[R * D + r]);
+    const float mz = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t k = c - 1; k <= last; ++k) {
+      const float* s = SeqSlot<R, D>::at(ws, seq_slot_of(k, k != c - 1));
+      const float f = seq_ex2(s[R * D + r] - mz);
+      const float4 x = *reinterpret_cast<const float4*>(s + r * D + d);
+      l += f * s[R * D + R + r];
+      o.x += f * x.x;
+      o.y += f * x.y;
+      o.z += f * x.z;
+      o.w += f * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no piece saw a key
+    const int64_t row = (w.u.q_begin + (r0 + r) / w.group) * a.q_heads + w.u.h * w.group + (r0 + r) % w.group;
+    *reinterpret_cast<uint2*>(O + row * D + d) =
+        make_uint2(Half16<T>::pack2(o.x * inv, o.y * inv), Half16<T>::pack2(o.z * inv, o.w * inv));
+    if (lse && d == 0) lse[row] = l == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(l));
+  }
+}
+
+}  // namespace wk

@@ -8,6 +8,8 @@
 #include "common.cuh"
 #include "host.cuh"
 #include "seq.cuh"
+#include "seq_cache.cuh"
+#include "seq_rows.cuh"
 
 using namespace wk;
 
@@ -20,8 +22,9 @@ bool seq_d_ok(int d) { return d == 32 || d == 64 || d == 128 || d == 160; }
 bool type16(wk_dtype t) { return t == WK_BF16 || t == WK_F16; }
 bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// The largest number of rows a tensor may have: byte offsets stay far inside 64 bits.
-constexpr int64_t kMaxRows = int64_t{1} << 40;
+// The largest number of rows a tensor may have (offsets are int32), and the most rows (times
+// heads) or keys of one sequence: the kernels number those in 32 bits.
+constexpr int64_t kMaxRows = INT32_MAX, kMostRows = int64_t{1} << 30;
 
 // Stride in elements from token to token: 0 means dense.
 int64_t stride_of(int64_t s, int heads, int d) { return s == 0 ? static_cast<int64_t>(heads) * d : s; }
@@ -39,7 +42,7 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
 wk_status check_config(const wk_xattn_config* c) {
   if (!c || c->batch < 0 || c->q_heads < 1 || c->kv_heads < 1 || c->q_heads % c->kv_heads != 0 || c->max_q < 0 ||
       c->max_kv < 0 || c->total_q < 0 || c->total_kv < 0 || c->total_q > kMaxRows || c->total_kv > kMaxRows ||
-      !(c->scale >= 0.f) || !std::isfinite(c->scale))
+      c->max_kv > kMostRows || static_cast<int64_t>(c->max_q) * c->q_heads > kMostRows || !(c->scale >= 0.f) || !std::isfinite(c->scale))
     return WK_ERR_INVALID_ARG;
   if (!seq_d_ok(c->d) || !type16(c->dtype) || c->q_heads > 1024) return WK_ERR_UNSUPPORTED;
   const int64_t qs = stride_of(c->q_stride, c->q_heads, c->d), ks = stride_of(c->k_stride, c->kv_heads, c->d),
@@ -97,6 +100,57 @@ void cache_args(SeqArgs* a, const wk_cache& c, const int32_t* table, int32_t wid
   a->v_exp = c.V_exp;
 }
 
+// ---------------------------------------------------------------- launches
+
+// A kernel that may start while the one before it on the stream ends (it waits for its results
+// itself).
+template <typename... P, typename... A>
+wk_status launch_dependent(void (*fn)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, P(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return WK_ERR_CUDA;
+  }
+  return WK_OK;
+}
+
+// ---- the few-rows kernel: packed rows per (sequence, key head) up to 16 (seq_rows.cuh)
+constexpr int kSMs = 148;  // the grids' unit; results do not depend on it
+constexpr int kRowsMost = 16, kRowsKB = 128;
+
+int64_t packed_rows(const SeqArgs& a) { return static_cast<int64_t>(a.max_q) * (a.q_heads / a.kv_heads); }
+int rows_nq(const SeqArgs& a) { return packed_rows(a) <= 8 ? 1 : 2; }
+int rows_pieces(int d, int nq) { return kSMs * seq_rows_occupancy(d, nq); }
+
+// Bytes of partial results; none where no sequence has more than one key block.
+int64_t rows_ws(const SeqArgs& a, int d) {
+  if (a.max_kv <= kRowsKB) return 0;
+  const int nq = rows_nq(a);
+  return int64_t{4} * 2 * rows_pieces(d, nq) * 8 * nq * (d + 2);
+}
+
+template <int D, typename T, int SRC, int NQ>
+wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* lse, float* ws, const SeqArgs& a,
+                   cudaStream_t st) {
+  const int64_t pieces = rows_pieces(D, NQ);
+  seq_rows_kernel<D, T, SRC, NQ><<<static_cast<unsigned>(pieces), SEQ_ROWS_THREADS, 0, st>>>(
+      static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse, ws, a, pieces);
+  const wk_status s = launch_status();
+  if (s != WK_OK || a.max_kv <= kRowsKB) return s;
+  return launch_dependent(seq_combine_kernel<8 * NQ, kRowsKB, D, SRC, T>, static_cast<unsigned>(pieces - 1),
+                          SEQ_COMBINE_THREADS, st, ws, static_cast<T*>(O), lse, a, pieces);
+}
+
+int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : 0; }
+
 constexpr int kWarps = 8;
 bool grid_of(int64_t warps, unsigned* grid) {
   const int64_t g = (warps + kWarps - 1) / kWarps;
@@ -122,11 +176,16 @@ struct RunForward {
   const void *Q, *K, *V;
   void* O;
   float* lse;
+  float* ws;
   SeqArgs a;
   int src;
   cudaStream_t st;
   template <int D, typename T, int SRC>
   wk_status run() const {
+    if (packed_rows(a) <= kRowsMost)
+      return rows_nq(a) == 1
+                 ? run_rows<D, T, SRC, 1>(Q, K, V, O, lse, ws, a, st)
+                 : run_rows<D, T, SRC, 2>(Q, K, V, O, lse, ws, a, st);
     unsigned grid;
     if (!grid_of(static_cast<int64_t>(a.batch) * a.max_q * a.q_heads, &grid)) return WK_ERR_UNSUPPORTED;
     xattn_forward_kernel<D, T, SRC><<<grid, 32 * kWarps, 0, st>>>(static_cast<const T*>(Q), K, V, static_cast<T*>(O),
@@ -169,14 +228,16 @@ struct RunWrite {
   const void *K, *V;
   SeqArgs a;
   unsigned grid;
+  int32_t chunks;
   cudaStream_t st;
   template <int D, typename T>
   wk_status operator()() const {
     const T *k = static_cast<const T*>(K), *v = static_cast<const T*>(V);
     if (c.dtype == WK_E4M3)
-      cache_write_kernel<D, T, true><<<grid, 32 * kWarps, 0, st>>>(k, v, c.K, c.V, c.K_exp, c.V_exp, a);
+      cache_write_kernel<D, T, true><<<grid, SEQ_COPY_THREADS, 0, st>>>(k, v, c.K, c.V, c.K_exp, c.V_exp, a, chunks);
     else
-      cache_write_kernel<D, T, false><<<grid, 32 * kWarps, 0, st>>>(k, v, c.K, c.V, nullptr, nullptr, a);
+      cache_write_kernel<D, T, false>
+          <<<grid, SEQ_COPY_THREADS, 0, st>>>(k, v, c.K, c.V, nullptr, nullptr, a, chunks);
     return launch_status();
   }
 };
@@ -186,12 +247,15 @@ struct RunRead {
   void *K, *V;
   SeqArgs a;
   unsigned grid;
+  int32_t chunks;
   cudaStream_t st;
   template <int D, typename T>
   wk_status operator()() const {
     T *k = static_cast<T*>(K), *v = static_cast<T*>(V);
-    if (c.dtype == WK_E4M3) cache_read_kernel<D, T, 2><<<grid, 32 * kWarps, 0, st>>>(c.K, c.V, k, v, a);
-    else cache_read_kernel<D, T, 1><<<grid, 32 * kWarps, 0, st>>>(c.K, c.V, k, v, a);
+    if (c.dtype == WK_E4M3)
+      cache_read_kernel<D, T, SEQ_PAGED8><<<grid, SEQ_COPY_THREADS, 0, st>>>(c.K, c.V, k, v, a, chunks);
+    else
+      cache_read_kernel<D, T, SEQ_PAGED16><<<grid, SEQ_COPY_THREADS, 0, st>>>(c.K, c.V, k, v, a, chunks);
     return launch_status();
   }
 };
@@ -204,7 +268,7 @@ wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* 
   if (!bytes) return WK_ERR_INVALID_ARG;
   const wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
-  *bytes = backward ? cfg->total_q * cfg->q_heads * 4 : 0;
+  *bytes = backward ? cfg->total_q * cfg->q_heads * 4 : forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
   return WK_OK;
 }
 
@@ -232,7 +296,7 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cfg->d, cfg->dtype, RunForward{Q, K, V, O, lse, a, 0, reinterpret_cast<cudaStream_t>(stream)});
+  return with_type(cfg->d, cfg->dtype, RunForward{Q, K, V, O, lse, static_cast<float*>(workspace), a, 0, reinterpret_cast<cudaStream_t>(stream)});
 }
 
 wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V, const void* O,
@@ -297,13 +361,15 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
     return WK_ERR_INVALID_ARG;
   SeqArgs a = make_args(cfg, new_off, nullptr, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
-  unsigned grid;
-  if (!grid_of(static_cast<int64_t>(batch) * max_new * cache->kv_heads * 2, &grid)) return WK_ERR_UNSUPPORTED;
+  const int32_t chunks = (max_new + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
+  const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
+  if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cache->d, dtype, RunWrite{*cache, K, V, a, grid, reinterpret_cast<cudaStream_t>(stream)});
+  return with_type(cache->d, dtype, RunWrite{*cache, K, V, a, static_cast<unsigned>(grid), chunks,
+                                                 reinterpret_cast<cudaStream_t>(stream)});
 }
 
 wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t table_width, const int32_t* kv_lens,
@@ -322,13 +388,15 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
   SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
-  unsigned grid;
-  if (!grid_of(static_cast<int64_t>(batch) * max_kv * cache->kv_heads * 2, &grid)) return WK_ERR_UNSUPPORTED;
+  const int32_t chunks = (max_kv + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
+  const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
+  if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cache->d, dtype, RunRead{*cache, K, V, a, grid, reinterpret_cast<cudaStream_t>(stream)});
+  return with_type(cache->d, dtype, RunRead{*cache, K, V, a, static_cast<unsigned>(grid), chunks,
+                                                reinterpret_cast<cudaStream_t>(stream)});
 }
 
 wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xattn_config* cfg, int64_t* bytes) {
@@ -339,7 +407,7 @@ wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xattn_con
   if (s != WK_OK) return s;
   if (cfg->kv_heads != cache->kv_heads || cfg->d != cache->d) return WK_ERR_INVALID_ARG;
   if (cache->dtype != WK_E4M3 && cache->dtype != cfg->dtype) return WK_ERR_UNSUPPORTED;
-  *bytes = 0;
+  *bytes = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
   return WK_OK;
 }
 
@@ -364,8 +432,8 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cfg->d, cfg->dtype, RunForward{Q, cache->K, cache->V, O, lse, a, cache->dtype == WK_E4M3 ? 2 : 1,
-                                                  reinterpret_cast<cudaStream_t>(stream)});
+  return with_type(cfg->d, cfg->dtype, RunForward{Q, cache->K, cache->V, O, lse, static_cast<float*>(workspace), a,
+                                                  cache->dtype == WK_E4M3 ? 2 : 1, reinterpret_cast<cudaStream_t>(stream)});
 }
 
 }  // extern "C"

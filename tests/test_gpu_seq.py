@@ -361,6 +361,8 @@ CACHED = [
     ([200], [900], 2, 2, 160, 64),
     ([300, 5], [300, 1200], 8, 1, 64, 16),
     ([129], [129], 3, 3, 32, 128),
+    ([2, 1, 3], [700, 300, 3], 4, 1, 128, 64),
+    ([3, 2], [1111, 15], 5, 1, 160, 32),
 ]
 
 
@@ -419,6 +421,27 @@ def test_more_new_tokens_than_positions_leaves_rows_empty():
     _ok()
     _check_attend(c, q, [5, 1], O, L, True)
     assert (O[:3] == 0).all() and torch.isinf(L[:3]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("d", [32, 160])
+def test_small_values_of_8_bit_rows(d, n, dt):
+    """Rows that hold nothing but e4m3's values below its normal range, rows of zeros with the least exponent, and
+    exponents far apart."""
+    gen = torch.Generator().manual_seed(6)
+    c = Cached([300, 40], 1, d, dt, 16, 8)
+    for name in ("K", "V"):
+        raw = c.cache[name].view(torch.uint8)
+        raw[:, :, ::2] = (raw[:, :, ::2] & 0x80) | (raw[:, :, ::2] & 0x07)
+        raw[:, :, 5] = 0
+        c.cache[name + "_exp"][:, :, 5] = 0
+        c.cache[name + "_exp"][:, :, ::2] += 9
+    c.cache["V_exp"][:, :, 11] = 100
+    q = _rand(gen, c.dt, n + 1, 2, d)
+    O, L = _attend(c, q, U.offsets([n, 1]), n, True)
+    _ok()
+    _check_attend(c, q, [n, 1], O, L, True)
 
 
 @pytest.mark.parametrize("n", [1, 70])
