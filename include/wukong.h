@@ -530,7 +530,8 @@ typedef struct {
 } wk_xattn_config;
 
 /* Bytes of device workspace that wk_xattn_forward (backward == 0) or wk_xattn_backward
- * (backward != 0) needs for this configuration; 0 if none. The workspace is the caller's: calls
+ * (backward != 0; then it is enough for the forward of the same step too) needs for this
+ * configuration; 0 if none. The workspace is the caller's: calls
  * that may run at the same time (other streams, graphs replayed side by side) need one each. It
  * need not be initialised and carries nothing from call to call. Needs no device. Errors:
  * WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED as wk_xattn_forward. */

@@ -57,56 +57,12 @@ __device__ __forceinline__ SeqRows<D, T, SRC> seq_rows(const SeqArgs& a, const v
   return {base, ex, stride, begin, SRC ? a.table + b * a.table_width : nullptr, h};
 }
 
-// ---------------------------------------------------------------- forward
-
 template <int D>
 __device__ __forceinline__ float seq_dot(const float (&x)[D / 32], const float (&y)[D / 32]) {
   float s = 0.f;
 #pragma unroll
   for (int c = 0; c < D / 32; ++c) s = fmaf(x[c], y[c], s);
   return warp_sum(s);
-}
-
-// One warp per (query row, query head).
-template <int D, typename T, int SRC>
-__global__ void xattn_forward_kernel(const T* __restrict__ Q, const void* K, const void* V, T* __restrict__ O,
-                                     float* __restrict__ lse, SeqArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t per_seq = static_cast<int64_t>(a.max_q) * a.q_heads;
-  const int64_t b = unit / per_seq;
-  if (b >= a.batch) return;
-  const int i = static_cast<int>(unit % per_seq / a.q_heads), h = static_cast<int>(unit % a.q_heads);
-  const SeqSpan q = seq_span(a.q_off, nullptr, b, a.total_q, a.max_q);
-  const SeqSpan kv = seq_keys<SRC>(a, b);
-  if ((q.bad || kv.bad) && lane == 0) flag_error(a.status, kFlagBadShape);
-  if (i >= q.len) return;
-  const int hk = h / (a.q_heads / a.kv_heads);
-  const auto kr = seq_rows<D, T, SRC>(a, K, a.k_exp, a.k_stride, b, kv.begin, hk);
-  const auto vr = seq_rows<D, T, SRC>(a, V, a.v_exp, a.v_stride, b, kv.begin, hk);
-  const int seen = seq_seen(kv.len, q.len, i, a.causal);
-  float x[D / 32], o[D / 32], y[D / 32], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    x[c] = Half16<T>::to(Q[(q.begin + i) * a.q_stride + h * D + c * 32 + lane]);
-    o[c] = 0.f;
-  }
-  for (int j = 0; j < seen; ++j) {
-    if (!kr.load(a, j, lane, y)) continue;
-    const float s = seq_dot<D>(x, y) * a.scale;
-    const float mn = fmaxf(m, s);
-    const float f = expf(m - mn), p = expf(s - mn);
-    if (!vr.load(a, j, lane, y)) continue;
-    l = l * f + p;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) o[c] = o[c] * f + p * y[c];
-    m = mn;
-  }
-  const float inv = seen > 0 ? 1.f / l : 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    O[((q.begin + i) * a.q_heads + h) * D + c * 32 + lane] = Half16<T>::from(o[c] * inv);
-  if (lse && lane == 0) lse[(q.begin + i) * a.q_heads + h] = m + logf(l);
 }
 
 // ---------------------------------------------------------------- backward

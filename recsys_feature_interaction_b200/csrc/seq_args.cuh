@@ -8,7 +8,8 @@
 // thread block: no block has more than ceil(T / grid) key blocks to do, however ragged the batch and
 // however few its rows, and which block does what depends on the lengths alone. A unit that a cut
 // goes through is finished by the combine kernel from fp32 partial results: piece c leaves those of
-// the unit it enters in the middle in slot 2c, those of the unit it leaves unfinished in slot 2c + 1.
+// the unit it enters in the middle in slot 2c, those of the unit it leaves unfinished in slot 2c + 1,
+// and a note about the latter.
 #pragma once
 
 #include "common.cuh"
@@ -225,58 +226,93 @@ struct SeqWalk {
   }
 };
 
-// fp32 partial results of a piece of a unit: O [R, D] not normalised, then m [R] (base 2), l [R].
-template <int R, int D>
-struct SeqSlot {
-  static constexpr int64_t kFloats = static_cast<int64_t>(R) * (D + 2);
-  static __device__ __forceinline__ float* at(float* ws, int64_t slot) { return ws + slot * kFloats; }
+// Partial results in the workspace: a note per piece about the unit that it leaves unfinished (its
+// last one, if any), then two slots per piece. A slot holds, in fp32, the unit's O [R, D] not
+// normalised, in pieces of four columns ([D / 4][R][4], so that the rows of a warp lie next to each
+// other), then m [R] (base 2) and l [R].
+struct SeqNote {
+  int32_t rows, r0;       // packed rows of the unit (0: the piece leaves none unfinished), the first one
+  int32_t group, pieces;  // query heads per key head; pieces that the unit is spread over
+  int64_t q_begin;
+  int32_t h, pad[3];
 };
 
-__device__ __forceinline__ int64_t seq_slot_of(int64_t piece, bool enters) { return 2 * piece + (enters ? 0 : 1); }
+template <int R, int D>
+struct SeqSlots {
+  static constexpr int64_t kFloats = static_cast<int64_t>(R) * (D + 2);
+  static constexpr int64_t bytes(int64_t pieces) {
+    return pieces * static_cast<int64_t>(sizeof(SeqNote)) + 2 * pieces * kFloats * 4;
+  }
+  static __device__ __forceinline__ SeqNote* note(float* ws, int64_t piece) {
+    return reinterpret_cast<SeqNote*>(ws) + piece;
+  }
+  // the slot of the unit that piece enters in the middle, or of the one that it leaves unfinished
+  static __device__ __forceinline__ float* slot(float* ws, int64_t pieces, int64_t piece, bool enters) {
+    return reinterpret_cast<float*>(reinterpret_cast<SeqNote*>(ws) + pieces) + (2 * piece + (enters ? 0 : 1)) * kFloats;
+  }
+  static __device__ __forceinline__ float* o(float* slot, int r, int d) { return slot + (d / 4 * R + r) * 4 + d % 4; }
+  static __device__ __forceinline__ float* m(float* slot) { return slot + R * D; }
+  static __device__ __forceinline__ float* l(float* slot) { return slot + R * D + R; }
+};
 
-// Combines the pieces of cut units: block c does the unit that the cut before piece c goes through,
-// if that is the unit's first cut. m and l of a row that a piece saw no key of are -inf and 0.
-constexpr int SEQ_COMBINE_THREADS = 256;
-template <int R, int KB, int D, int SRC, typename T>
+// Every piece says what it leaves unfinished; by one thread, for a unit u of which the piece has
+// [j0, j1) with j0 == 0 and j1 < nb, or with none = true.
+template <int R, int D>
+__device__ __forceinline__ void seq_leave_note(float* ws, int64_t piece, const SeqUnit& u, int group, int64_t per,
+                                               bool none) {
+  SeqNote n;
+  n.rows = none ? 0 : min(R, u.rows - u.t * R);
+  n.r0 = u.t * R;
+  n.group = group;
+  // the unit's last key block lies nb - j1 blocks behind the piece's end
+  n.pieces = none ? 0 : 1 + static_cast<int32_t>((u.nb - u.j1 + per - 1) / per);
+  n.q_begin = u.q_begin;
+  n.h = u.h;
+  n.pad[0] = n.pad[1] = n.pad[2] = 0;
+  *SeqSlots<R, D>::note(ws, piece) = n;
+}
+
+// Joins the pieces of cut units. blockIdx.x = piece * (R / CR) + block of CR rows. m and l of a row
+// that a piece saw no key of are -inf and 0.
+constexpr int SEQ_COMBINE_THREADS = 128;
+template <int R, int CR, int D, typename T>
 __global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
-    seq_combine_kernel(float* ws, T* __restrict__ O, float* __restrict__ lse, SeqArgs a, int64_t pieces) {
-  __shared__ int64_t sh[SEQ_COMBINE_THREADS / 32 + 4];
-  const int64_t c = blockIdx.x + 1;
-  const SeqPlace p = seq_place<R, KB, SRC, SEQ_COMBINE_THREADS>(a, c, pieces, sh, false);
-  if (p.begin >= p.end) return;
-  SeqWalk<R, KB, SRC> w;
-  w.start(a, p);
-  if (w.u.j0 == 0) return;                       // the cut lies between two units
-  const int64_t f0 = p.begin - w.u.j0;           // the unit's place on the line
-  if (f0 / p.per != c - 1) return;               // an earlier cut is its first
-  const int nb = seq_tile_cost<R, KB>(a, w.u.n, w.u.len, w.group, w.u.t);
-  const int64_t last = (f0 + nb - 1) / p.per;
-  const int r0 = w.u.t * R, rows = min(R, w.u.rows - r0);
-#if __CUDA_ARCH__ >= 900
+    seq_combine_kernel(float* ws, T* __restrict__ O, float* __restrict__ lse, int32_t q_heads, int32_t pieces) {
+  using S = SeqSlots<R, D>;
+  const int32_t c = blockIdx.x / (R / CR);
+  const int first = (blockIdx.x % (R / CR)) * CR;
   cudaGridDependencySynchronize();
-#endif
-  for (int i = threadIdx.x; i < rows * (D / 4); i += SEQ_COMBINE_THREADS) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    float m = -INFINITY;
-    for (int64_t k = c - 1; k <= last; ++k)
-      m = fmaxf(m, SeqSlot<R, D>::at(ws, seq_slot_of(k, k != c - 1))[R * D + r]);
+  const SeqNote n = *S::note(ws, c);
+  if (first >= n.rows) return;
+  for (int i = threadIdx.x; i < CR * (D / 8); i += SEQ_COMBINE_THREADS) {
+    const int r = first + i % CR, d = (i / CR) * 8;
+    if (r >= n.rows) continue;
+    float* s0 = S::slot(ws, pieces, c, false);
+    float m = S::m(s0)[r];
+    for (int k = 1; k < n.pieces; ++k) m = fmaxf(m, S::m(S::slot(ws, pieces, c + k, true))[r]);
     const float mz = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t k = c - 1; k <= last; ++k) {
-      const float* s = SeqSlot<R, D>::at(ws, seq_slot_of(k, k != c - 1));
-      const float f = seq_ex2(s[R * D + r] - mz);
-      const float4 x = *reinterpret_cast<const float4*>(s + r * D + d);
-      l += f * s[R * D + R + r];
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
+    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < n.pieces; ++k) {
+      float* s = k == 0 ? s0 : S::slot(ws, pieces, c + k, true);
+      const float f = seq_ex2(S::m(s)[r] - mz);
+      const float4 x = *reinterpret_cast<const float4*>(S::o(s, r, d));
+      const float4 y = *reinterpret_cast<const float4*>(S::o(s, r, d + 4));
+      l += f * S::l(s)[r];
+      o[0] += f * x.x;
+      o[1] += f * x.y;
+      o[2] += f * x.z;
+      o[3] += f * x.w;
+      o[4] += f * y.x;
+      o[5] += f * y.y;
+      o[6] += f * y.z;
+      o[7] += f * y.w;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no piece saw a key
-    const int64_t row = (w.u.q_begin + (r0 + r) / w.group) * a.q_heads + w.u.h * w.group + (r0 + r) % w.group;
-    *reinterpret_cast<uint2*>(O + row * D + d) =
-        make_uint2(Half16<T>::pack2(o.x * inv, o.y * inv), Half16<T>::pack2(o.z * inv, o.w * inv));
+    const int pr = n.r0 + r;
+    const int64_t row = (n.q_begin + pr / n.group) * q_heads + n.h * n.group + pr % n.group;
+    *reinterpret_cast<uint4*>(O + row * D + d) =
+        make_uint4(Half16<T>::pack2(o[0] * inv, o[1] * inv), Half16<T>::pack2(o[2] * inv, o[3] * inv),
+                   Half16<T>::pack2(o[4] * inv, o[5] * inv), Half16<T>::pack2(o[6] * inv, o[7] * inv));
     if (lse && d == 0) lse[row] = l == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(l));
   }
 }

@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const float scale_log2 = a.scale * 1.4426950408889634f;
   const SeqPlace place = seq_place<R, C::KB, SRC, SEQ_ROWS_THREADS>(a, blockIdx.x, pieces, sh, blockIdx.x == 0);
-  if (place.begin >= place.end) return;
+  using S = SeqSlots<R, D>;
+  bool left = false;  // a unit left unfinished
   SeqWalk<R, C::KB, SRC> w;
   w.start(a, place);
   for (; w.next(a); w.advance(a)) {
@@ -410,7 +411,11 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     __syncthreads();
     const bool whole = u.j0 == 0 && u.j1 == u.nb;
     const int rows = min(R, u.rows - r0);
-    float* slot = whole ? nullptr : SeqSlot<R, D>::at(ws, seq_slot_of(blockIdx.x, u.j0 > 0));
+    float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
+    if (u.j0 == 0 && u.j1 < u.nb) {
+      left = true;
+      if (threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, u, group, place.per, false);
+    }
     for (int i = threadIdx.x; i < rows * (D / 4); i += SEQ_ROWS_THREADS) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
       float mm = sm_m[0][r];
@@ -436,15 +441,16 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
             make_uint2(Half16<T>::pack2(o.x * inv, o.y * inv), Half16<T>::pack2(o.z * inv, o.w * inv));
         if (lse && d == 0) lse[row] = ll == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(ll));
       } else {
-        *reinterpret_cast<float4*>(slot + r * D + d) = o;
+        *reinterpret_cast<float4*>(S::o(slot, r, d)) = o;
         if (d == 0) {
-          slot[R * D + r] = mm;
-          slot[R * D + R + r] = ll;
+          S::m(slot)[r] = mm;
+          S::l(slot)[r] = ll;
         }
       }
     }
     __syncthreads();
   }
+  if (ws && !left && threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, w.u, w.group, place.per, true);
 }
 
 }  // namespace wk

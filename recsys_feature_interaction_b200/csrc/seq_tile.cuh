@@ -1,0 +1,711 @@
+// seq_tile.cuh -- attention of more than 16 packed query rows per (sequence, key head) on the
+// 5th-generation tensor cores, over jagged tensors or a cache.
+//
+// A block holds 128 packed query rows (SeqUnit) and walks 128-key blocks: S = Q K^T with Q in TMEM
+// and the K tile K-major in shared memory, softmax weights from TMEM by two warps per lane quarter,
+// P written over S's columns, O += P V with the V tile MN-major. S is double-buffered, S of the
+// next block is issued before P V of this one, K and V tiles arrive in one ring in the order in
+// which the products use them (K0, K1, V0, K2, V1, ..).
+//
+// Roles: warp 0 lane 0 loads tiles with TMA (jagged: 128 rows from the sequence's first; a 16-bit
+// cache: one box per page); warp 1 issues the MMAs; warp 2 walks the block's units and hands them
+// to the other roles through a ring, so that none of them waits for offsets; warps 4 .. 11 run the
+// softmax; for an 8-bit cache warps 12 .. 15 load rows, convert them to the 16-bit type (exactly;
+// see seq_rows.cuh) and store them in the tiles' swizzled layout, in place of the TMA.
+//
+// Rows behind a sequence's last key belong to someone else: their scores are replaced by a select,
+// and their V rows, whose weights are 0, are overwritten with zeros in the tile before P V, because
+// 0 * NaN is NaN.
+//
+// The running maximum is raised only when a block exceeds it by more than 2^8; one weight in four
+// comes from a polynomial on the FMA pipe (whale.cuh).
+#pragma once
+
+#include "seq_args.cuh"
+#include "seq_rows.cuh"
+#include "whale.cuh"
+
+namespace wk {
+
+// Barrier over `count` threads that also tells every one of them whether `p` held for all.
+__device__ __forceinline__ bool named_bar_and(int id, int count, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0u;
+}
+
+// True for one thread of a converged warp, always the same one. The MMAs of a warp that runs as a
+// whole are issued under it: with a plain lane == 0 the compiler does not know that one thread is
+// left, and the tensor pipe falls behind when the softmax warps keep the issue slots busy (18 MMAs
+// of a block next to a softmax loop: 1630 cycles against 2240, 1306 with the SM to themselves).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
+}
+
+// max(a, b, c) and max(a, b) that give NaN if an operand is NaN.
+__device__ __forceinline__ float seq_max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float seq_max2(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// whale_ex2_poly with a floor whose result rounds to 0 in both 16-bit types, so that a masked score
+// (-inf) gets a weight of exactly 0: at x = -126.9997 the integer part is -127 and the polynomial
+// just above 1, so that adding -127 to its exponent leaves a subnormal below 2^-139.
+__device__ __forceinline__ float seq_ex2_poly(float x) {
+  x = fmaxf(x, -126.9997f);
+  const float t = x + 12582912.f;
+  const float f = x - (t - 12582912.f);
+  const float p = fmaf(fmaf(fmaf(0.05517158f, f, 0.24261111f), f, 0.69326103f), f, 0.99992806f);
+  return __uint_as_float(__float_as_uint(p) + (__float_as_uint(t) << 23));
+}
+
+template <int N>
+__device__ __forceinline__ float seq_max(const uint32_t (&v)[N]) {
+  float t[(N + 2) / 3];
+#pragma unroll
+  for (int i = 0; i < N / 3; ++i)
+    t[i] = seq_max3(__uint_as_float(v[3 * i]), __uint_as_float(v[3 * i + 1]), __uint_as_float(v[3 * i + 2]));
+  if constexpr (N % 3 == 1) t[N / 3] = __uint_as_float(v[N - 1]);
+  if constexpr (N % 3 == 2) t[N / 3] = seq_max2(__uint_as_float(v[N - 2]), __uint_as_float(v[N - 1]));
+  constexpr int M = (N + 2) / 3;
+  float a[4] = {t[0], t[1 % M], t[2 % M], t[3 % M]};
+#pragma unroll
+  for (int i = 4; i + 1 < M; i += 2) a[(i / 2) & 3] = seq_max3(a[(i / 2) & 3], t[i], t[i + 1]);
+  if constexpr (M > 4 && M % 2 == 1) a[0] = seq_max2(a[0], t[M - 1]);
+  return seq_max2(seq_max3(a[0], a[1], a[2]), a[3]);
+}
+
+template <int D_, int SRC_>
+struct StCfg {
+  static constexpr int D = D_, SRC = SRC_;
+  static constexpr int R = 128, KB = 128;
+  static constexpr int BW = (D % 64 == 0) ? 64 : 32;     // columns per box
+  static constexpr int SWB = BW * 2;                     // bytes per box row = swizzle span
+  static constexpr uint32_t SWMODE = BW == 64 ? 2u : 4u;
+  static constexpr int NBOX = D / BW;
+  static constexpr int BOXB = KB * SWB;
+  static constexpr int TILEB = NBOX * BOXB;              // one K or V tile
+  static constexpr int LIMIT = 227 * 1024;
+  static constexpr int NU = 4;                           // units in flight between the walker and the roles
+  static constexpr int BARB = 512;                       // barriers, TMEM address, references
+  static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
+  static constexpr int REDB = 4 * R * 4;                 // softmax pair exchange [2 parities][2 halves][R]
+  static constexpr int FIXED = BARB + UNITB + REDB;
+  static constexpr int STAGES_RAW = (LIMIT - FIXED) / TILEB;
+  static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+  // more than half an SM's shared memory: one block per SM, whose 512 TMEM columns are its own
+  static constexpr int SMEM = FIXED + STAGES * TILEB > 120 * 1024 ? FIXED + STAGES * TILEB : 120 * 1024;
+  // TMEM: S0, S1 [0, 256) (P over their first 64 columns), O [256, 256 + D), Q behind it
+  static constexpr int OCOL = 2 * KB;
+  static constexpr int QCOL = OCOL + D;
+  static constexpr int THREADS = SRC == SEQ_PAGED8 ? 512 : 384;
+  static constexpr int LOADERS = 128;
+  static_assert(QCOL + D / 2 <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
+  static_assert((2 * STAGES + 9 + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
+};
+
+// Key blocks [j0, j1) of a unit that hold keys (a unit without keys has a cost, but no block).
+__device__ __forceinline__ int seq_real_end(const SeqArgs& a, const SeqUnit& u, int group, int R, int KB) {
+  const int last = (min((u.t + 1) * R, u.rows) - 1) / group;
+  return min(u.j1, (seq_seen(u.len, u.n, last, a.causal) + KB - 1) / KB);
+}
+
+template <int D, typename T, int SRC>
+__global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
+    seq_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const T* __restrict__ Q, const void* __restrict__ K8, const void* __restrict__ V8,
+                    T* __restrict__ O, float* __restrict__ lse, float* __restrict__ ws, SeqArgs a, int64_t pieces) {
+  using C = StCfg<D, SRC>;
+  constexpr int R = C::R, KB = C::KB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if ((smem_u32(smem_raw) & 1023u) != 0u) {  // the swizzled layout needs 1024-byte alignment
+    if (threadIdx.x == 0) flag_error(a.status, kFlagBadShape);
+    return;
+  }
+  uint8_t* tiles = smem_raw;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::TILEB);
+  uint64_t* kv_full = bars;                  // [STAGES] tile landed
+  uint64_t* kv_empty = bars + C::STAGES;     // [STAGES] its product has read it
+  uint64_t* s_full = bars + 2 * C::STAGES;   // [2] S in TMEM
+  uint64_t* p_full = s_full + 2;             // [2] P in TMEM
+  uint64_t* p_empty = s_full + 4;            // [2] P V has read it (so O holds that block)
+  uint64_t* q_full = s_full + 6;             // the unit's Q rows are in TMEM
+  uint64_t* o_empty = s_full + 7;            // O read by the softmax warps (per unit)
+  uint64_t* fin = s_full + 8;
+  uint64_t* u_full = s_full + 9;             // [NU] unit handed over
+  uint64_t* u_empty = u_full + C::NU;        // [NU] every role is done with it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + C::NU);
+  int32_t* refs = reinterpret_cast<int32_t*>(tmem_slot + 4);  // [NU][2] exponent references of K and V
+  SeqUnit* unit = reinterpret_cast<SeqUnit*>(tiles + C::STAGES * C::TILEB + C::BARB);
+  float* red = reinterpret_cast<float*>(tiles + C::STAGES * C::TILEB + C::BARB + C::UNITB);
+  int32_t* shared_top = refs + 2 * C::NU;                // [2][4] the loaders' maxima
+  unsigned* status = a.status;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    if (SRC != SEQ_PAGED8) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&kv_full[s], SRC == SEQ_PAGED8 ? C::LOADERS / 32 : 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);
+      mbar_init(&p_empty[i], 1);
+    }
+    mbar_init(q_full, 8);
+    mbar_init(o_empty, 8);
+    mbar_init(fin, 1);
+    for (int i = 0; i < C::NU; ++i) {
+      mbar_init(&u_full[i], 1);
+      mbar_init(&u_empty[i], 9 + (SRC == SEQ_PAGED8 ? C::LOADERS / 32 : 1));
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  const SeqPlace place = seq_place<R, KB, SRC, C::THREADS>(a, blockIdx.x, pieces, reinterpret_cast<int64_t*>(red), blockIdx.x == 0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int group = a.q_heads / a.kv_heads;
+
+  // The roles' side of the unit ring: the next unit, or false behind the last (b < 0).
+  uint32_t ui = 0;
+  auto unit_take = [&](SeqUnit& u) -> bool {
+    const uint32_t s = ui % C::NU;
+    if (!mbar_wait(&u_full[s], (ui / C::NU) & 1u, status)) return false;
+    u = unit[s];
+    return u.b >= 0;
+  };
+  auto unit_done = [&]() {  // by one thread per warp
+    mbar_arrive(&u_empty[ui % C::NU]);
+  };
+
+  if (warp == 2) {
+    // -------------------------------------------------------------- walker
+    if (lane == 0) {
+      SeqWalk<R, KB, SRC> w;
+      w.start(a, place);
+      bool left = false;  // a unit left unfinished
+      for (;;) {
+        const bool more = w.next(a);
+        const uint32_t s = ui % C::NU;
+        if (!mbar_wait(&u_empty[s], ((ui / C::NU) & 1u) ^ 1u, status)) break;
+        if (!more) w.u.b = -1;
+        unit[s] = w.u;
+        mbar_arrive(&u_full[s]);
+        ++ui;
+        if (!more) break;
+        if (ws && w.u.j0 == 0 && w.u.j1 < w.u.nb) {
+          left = true;
+          seq_leave_note<R, D>(ws, blockIdx.x, w.u, group, place.per, false);
+        }
+        w.advance(a);
+      }
+      if (ws && !left) seq_leave_note<R, D>(ws, blockIdx.x, w.u, group, place.per, true);
+    }
+  } else if (warp == 0 && SRC != SEQ_PAGED8) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      SeqUnit u;
+      auto load = [&](const CUtensorMap* tm, int j) -> bool {
+        if (!mbar_wait(&kv_empty[s], ph ^ 1u, status)) return false;
+        uint8_t* dst = tiles + s * C::TILEB;
+        if constexpr (SRC == SEQ_JAGGED) {
+          mbar_arrive_expect_tx(&kv_full[s], static_cast<uint32_t>(C::TILEB));
+#pragma unroll
+          for (int bx = 0; bx < C::NBOX; ++bx)
+            tma_load_3d(tm, &kv_full[s], dst + bx * C::BOXB, bx * C::BW, u.h, static_cast<int32_t>(u.kv_begin) + j * KB);
+        } else {
+          const int ps = 1 << a.page_shift;
+          const int32_t* row = a.table + static_cast<int64_t>(u.b) * a.table_width;
+          const int valid = min(KB, u.len - j * KB), np = (valid + ps - 1) >> a.page_shift;
+          int32_t page[8];
+          int good = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            page[i] = -1;
+            if (i < np) {
+              page[i] = seq_page(row, static_cast<int64_t>(j) * KB + i * ps, a.page_shift, a.num_pages);
+              if (page[i] < 0) flag_error(status, kFlagBadShape);
+              else ++good;
+            }
+          }
+          mbar_arrive_expect_tx(&kv_full[s], static_cast<uint32_t>(good * ps * D * 2));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (page[i] < 0) continue;
+            const int32_t r = static_cast<int32_t>(((static_cast<int64_t>(page[i]) * a.kv_heads + u.h) << a.page_shift));
+#pragma unroll
+            for (int bx = 0; bx < C::NBOX; ++bx)
+              tma_load_2d(tm, &kv_full[s], dst + bx * C::BOXB + i * ps * C::SWB, bx * C::BW, r);
+          }
+        }
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+        return true;
+      };
+      while (ok && unit_take(u)) {
+        const int j1 = seq_real_end(a, u, group, R, KB);
+        for (int j = u.j0; ok && j < j1; ++j) {
+          if (j == u.j0) ok = load(&tmK, j);
+          if (ok && j + 1 < j1) ok = load(&tmK, j + 1);
+          if (ok) ok = load(&tmV, j);
+        }
+        unit_done();
+        ++ui;
+      }
+      // copies already issued must land before the block exits (a failed wait left some behind)
+      if (status_set(status))
+        for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    // The whole warp walks; one thread issues. The MMAs of a thread run in issue order, so S of block
+    // j + 2 is written into S_j's columns only after P V_j, issued before it, has read P_j there.
+    const bool bf = Half16<T>::kBF16;
+    const uint32_t idS = idesc_f16kind_f32(R, KB, 0, 0, bf);
+    const uint32_t idO = idesc_f16kind_f32(R, D, 0, 1, bf);
+    int s = 0;
+    uint32_t ph = 0, g = 0, uc = 0;
+    bool ok = true;
+    SeqUnit u;
+    auto step = [&]() {
+      if (++s == C::STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
+    };
+    auto issue_s = [&](uint32_t gb) -> bool {
+      if (!mbar_wait(&kv_full[s], ph, status)) return false;
+      if (elect_one()) {
+        tc_fence_after();
+        const uint32_t ka = smem_u32(tiles + s * C::TILEB);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
+          const uint64_t bd = smem_desc(ka + bx * C::BOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
+          whale_umma_ts(tmem + (gb & 1u) * KB, tmem + C::QCOL + ks * 8, bd, idS, ks != 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[gb & 1u]);
+        umma_commit(&kv_empty[s]);
+      }
+      __syncwarp();
+      step();
+      return true;
+    };
+    auto issue_pv = [&](int j, bool last, uint32_t gj, bool first) -> bool {
+      if (!mbar_wait(&kv_full[s], ph, status)) return false;
+      const uint32_t va = smem_u32(tiles + s * C::TILEB);
+      const int valid = u.len - j * KB;
+      if (SRC != SEQ_PAGED8 && last && valid < KB) {  // rows behind the sequence: their weights are 0
+        for (int i = lane; i < (KB - valid) * C::NBOX * (C::SWB / 16); i += 32) {
+          const int r = valid + i / (C::NBOX * (C::SWB / 16)), x = i % (C::NBOX * (C::SWB / 16));
+          uint8_t* p = tiles + s * C::TILEB + (x / (C::SWB / 16)) * C::BOXB + r * C::SWB + (x % (C::SWB / 16)) * 16;
+          *reinterpret_cast<uint4*>(p) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!mbar_wait(&p_full[gj & 1u], (gj >> 1) & 1u, status)) return false;
+      if (elect_one()) {
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < KB / 16; ++ks) {
+          // MN-major V: BW-column atoms BOXB apart, 8-key groups 8 * SWB apart
+          const uint64_t bd = smem_desc(va + ks * 16 * C::SWB, C::BOXB, 8 * C::SWB, C::SWMODE);
+          whale_umma_ts(tmem + C::OCOL, tmem + (gj & 1u) * KB + ks * 8, bd, idO, (!first || ks) ? 1u : 0u);
+        }
+        umma_commit(&p_empty[gj & 1u]);
+        umma_commit(&kv_empty[s]);
+      }
+      __syncwarp();
+      step();
+      return true;
+    };
+    while (ok && unit_take(u)) {
+      const int j1 = seq_real_end(a, u, group, R, KB);
+      if (u.j0 < j1) {
+        ok = mbar_wait(q_full, uc & 1u, status);
+        if (ok) ok = issue_s(g);
+        for (int j = u.j0; ok && j < j1; ++j) {
+          if (j + 1 < j1) ok = issue_s(g + 1u);
+          // O is free once the softmax warps have read the unit before
+          if (ok && j == u.j0 && uc > 0) ok = mbar_wait(o_empty, (uc - 1u) & 1u, status);
+          if (ok) ok = issue_pv(j, j + 1 == j1, g, j == u.j0);
+          ++g;
+        }
+        ++uc;
+      }
+      __syncwarp();
+      if (lane == 0) unit_done();
+      ++ui;
+    }
+    __syncwarp();
+    if (elect_one()) {
+      umma_commit(fin);  // no MMA may still write TMEM when it is freed
+      mbar_drain(fin, 0u, status);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------- softmax
+    // Two warps per TMEM lane quarter: rows 32 q .. + 31, key columns 64 half .. + 63 of each
+    // block. The pair exchanges per-row partial maxima (by block parity) and, at the end of a
+    // unit, partial row sums, through shared memory under 64-thread barriers.
+    const int q = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const int row = q * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    const int bar_id = 1 + q;
+    uint32_t g = 0;
+    // After a failed wait a thread stops waiting but walks the unit to its end, so that the
+    // warp-collective TMEM accesses and the pair barriers stay converged; the pair leaves together.
+    bool ok = true;
+    SeqUnit u;
+    for (;;) {
+      const bool got = ok && unit_take(u);
+      if (!named_bar_and(bar_id, 64, got)) break;
+      __syncwarp();
+      const int j1 = seq_real_end(a, u, group, R, KB);
+      const int r = u.t * R + row;  // packed row of the sequence
+      const bool warp_on = u.t * R + q * 32 < u.rows;
+      const bool row_on = r < u.rows;
+      const int qi = row_on ? r / group : 0, qh = u.h * group + (row_on ? r % group : 0);
+      const int seen = row_on ? seq_seen(u.len, u.n, qi, a.causal) : INT32_MAX;
+      const bool whole = u.j0 == 0 && u.j1 == u.nb;
+      const int64_t orow = (u.q_begin + qi) * a.q_heads + qh;
+      if (u.j0 < j1) {
+        // the unit's query rows into TMEM (this half's D / 2 columns, as 16-bit pairs)
+        {
+          uint32_t qv[D / 4];
+          if (row_on) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(Q + (u.q_begin + qi) * a.q_stride + qh * D + half * (D / 2));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint4 v = __ldg(src + i);
+              qv[4 * i] = v.x;
+              qv[4 * i + 1] = v.y;
+              qv[4 * i + 2] = v.z;
+              qv[4 * i + 3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 4; ++i) qv[i] = 0u;
+          }
+          whale_tmem_st_cols<D / 4>(tmem + lane_base + C::QCOL + half * (D / 4), qv);
+          whale_tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_full);
+        }
+        float m = -INFINITY, l = 0.f;
+        float scale_log2 = a.scale * 1.4426950408889634f;
+        for (int j = u.j0; j < j1; ++j, ++g) {
+          const uint32_t buf = g & 1u;
+          if (ok) ok = mbar_wait(&s_full[buf], (g >> 1) & 1u, status);
+          tc_fence_after();
+          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16 && j == u.j0)  // known once the first K tile is
+            scale_log2 = a.scale * 1.4426950408889634f * seq_ex2(static_cast<float>(refs[2 * (ui % C::NU)] - 127));
+          uint32_t sr[KB / 2];
+          if (warp_on) {
+            const uint32_t ta = tmem + lane_base + buf * KB + half * (KB / 2);
+            tmem_ld32(ta, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            tmem_ld32(ta + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            tmem_ld_wait();
+          }
+          const int kvalid = seen - j * KB - half * (KB / 2);  // this row's keys in this half
+          if (!__all_sync(0xffffffffu, kvalid >= KB / 2)) {
+#pragma unroll
+            for (int c = 0; c < KB / 2; ++c)
+              if (c >= kvalid) sr[c] = 0xFF800000u;  // -inf
+          }
+          // P = 2^(S scale_log2 - m), rounded to the operand type and packed; row sum in fp32. From
+          // the second block of a row on it is computed with the running maximum at once, next to
+          // this block's maximum, and again only if that raises it.
+          const bool spec = j > u.j0;
+          uint32_t pk[KB / 4];
+          float lsum = 0.f, mb = -INFINITY, mnew = m, factor = 1.f;
+          bool redo = false;
+          bool again = warp_on && spec;
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {
+            if (again) {
+              const float nm = mnew == -INFINITY ? 0.f : -mnew;
+              float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int c2 = 0; c2 < KB / 4; ++c2) {
+                const float x0 = fmaf(__uint_as_float(sr[2 * c2]), scale_log2, nm);
+                const float x1 = fmaf(__uint_as_float(sr[2 * c2 + 1]), scale_log2, nm);
+                const float p0 = whale_ex2(x0);
+                const float p1 = (c2 & 1) ? seq_ex2_poly(x1) : whale_ex2(x1);
+                s4[(2 * c2) & 3] += p0;
+                s4[(2 * c2 + 1) & 3] += p1;
+                pk[c2] = Half16<T>::pack2(p0, p1);
+              }
+              lsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            }
+            if (pass == 1) break;
+            const float mh = seq_max<KB / 2>(sr);
+            red[(buf * 2 + half) * R + row] = mh;
+            // after this barrier both warps of the pair have read S_j: P_j may overwrite it
+            tc_fence_before();
+            named_bar(bar_id, 64);
+            tc_fence_after();
+            mb = seq_max2(mh, red[(buf * 2 + (half ^ 1)) * R + row]);
+            const float mb2 = mb * scale_log2;
+            const bool need = warp_on && row_on && (mb2 > m + 8.f);
+            if (need) {
+              mnew = mb2;
+              factor = whale_ex2(m - mnew);
+            }
+            redo = warp_on && (!spec || __any_sync(0xffffffffu, need));
+            if (!redo) break;
+            again = true;
+          }
+          if (mnew == -INFINITY) lsum = 0.f;  // no key seen yet
+          if (mb != mb) lsum = mb;  // a NaN score: the polynomial would lose it
+          // P V two blocks back has completed (keeps this waiter within one phase of p_empty)
+          if (ok) ok = mbar_wait(&p_empty[buf], ((g >> 1) & 1u) ^ 1u, status);
+          if (spec && redo) {
+            // the running maximum was raised: O must hold every earlier block before it is rescaled
+            const uint32_t gp = g - 1u;
+            if (ok) ok = mbar_wait(&p_empty[gp & 1u], (gp >> 1) & 1u, status);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = half; cc < D / 32; cc += 2) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+              whale_tmem_st32(tmem + lane_base + C::OCOL + cc * 32, o);
+            }
+          }
+          l = l * factor + lsum;
+          m = mnew;
+          // P_j over the first 64 columns of S_j: keys 64 half .. + 63 in columns 32 half .. + 31
+          if (warp_on) whale_tmem_st32(tmem + lane_base + buf * KB + half * 32, pk);
+          whale_tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[buf]);
+        }
+        // the row sums of both halves, through the exchange slot of the parity that the last block
+        // did not use; the second barrier keeps the next unit from overwriting it too early
+        const uint32_t gl = g - 1u;
+        float* red_sum = red + ((gl + 1u) & 1u) * 2 * R;
+        red_sum[half * R + row] = l;
+        named_bar(bar_id, 64);
+        const float lt = l + red_sum[(half ^ 1) * R + row];
+        named_bar(bar_id, 64);
+        if (ok) ok = mbar_wait(&p_empty[gl & 1u], (gl >> 1) & 1u, status);
+        tc_fence_after();
+        if (warp_on) {
+          float vs = 1.f;  // V's reference exponent
+          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
+            vs = seq_ex2(static_cast<float>(refs[2 * (ui % C::NU) + 1] - 127));
+          const float inv = whole ? (lt == 0.f ? 0.f : vs / lt) : vs;
+          using S = SeqSlots<R, D>;
+          float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
+#pragma unroll 1
+          for (int cc = half; cc < D / 32; cc += 2) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
+            tmem_ld_wait();
+            if (row_on && ok) {
+              if (whole) {
+                whale_st_row32<T>(O + orow * D + cc * 32, o, inv, nullptr);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
+                      make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                  __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+              }
+            }
+          }
+          if (row_on && half == 0) {
+            if (!whole) {
+              S::m(slot)[row] = m;
+              S::l(slot)[row] = lt;
+            } else if (lse) {
+              lse[orow] = lt == 0.f ? -INFINITY : 0.69314718055994531f * ((m == -INFINITY ? 0.f : m) + log2f(lt));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);
+      } else if (row_on) {  // no key: nothing to attend to
+        const uint32_t z[32] = {};
+#pragma unroll 1
+        for (int cc = half; cc < D / 32; cc += 2) whale_st_row32<T>(O + orow * D + cc * 32, z, 0.f, nullptr);
+        if (lse && half == 0) lse[orow] = -INFINITY;
+      }
+      __syncwarp();
+      if (lane == 0) unit_done();
+      ++ui;
+    }
+  } else if (SRC == SEQ_PAGED8 && warp >= 12) {
+    // --------------------------------------------- loaders of an 8-bit cache
+    constexpr int ITEMS = D / 16;  // 16-byte pieces of the tile per thread
+    const int tid = threadIdx.x - 384;
+    const int pmask = (1 << a.page_shift) - 1;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    SeqUnit u;
+    auto row_of = [&](const int32_t* trow, int k) -> int64_t {
+      const int page = seq_page(trow, k, a.page_shift, a.num_pages);
+      if (page < 0) {
+        flag_error(status, kFlagBadShape);
+        return -1;
+      }
+      return ((static_cast<int64_t>(page) * a.kv_heads + u.h) << a.page_shift) + (k & pmask);
+    };
+    for (;;) {
+      const bool got = ok && unit_take(u);
+      if (!named_bar_and(5, C::LOADERS, got)) break;
+      __syncwarp();
+      const int j1 = seq_real_end(a, u, group, R, KB);
+      const int32_t* trow = a.table + static_cast<int64_t>(u.b) * a.table_width;
+      int ref[2] = {127, 127};
+      if (!Half16<T>::kBF16 && u.j0 < j1) {
+        // fp16 cannot hold every power of two: rows are held relative to 2^7 below the piece's
+        // largest, which keeps all within 2^22 of it exact
+        int top[2] = {0, 0};
+        for (int k = u.j0 * KB + 16 * tid; k < min(u.len, j1 * KB); k += 16 * C::LOADERS) {
+          const int64_t r = row_of(trow, k);
+          if (r < 0) continue;
+          const uint4 e[2] = {__ldg(reinterpret_cast<const uint4*>(a.k_exp + r)),
+                              __ldg(reinterpret_cast<const uint4*>(a.v_exp + r))};
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int x = (reinterpret_cast<const uint32_t*>(&e[w])[i / 4] >> (8 * (i % 4))) & 255;
+              if (k + i < u.len && x != 255) top[w] = max(top[w], x);
+            }
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          top[w] = __reduce_max_sync(0xffffffffu, top[w]);
+          if (lane == 0) shared_top[w * 4 + (warp & 3)] = top[w];
+        }
+        named_bar(5, C::LOADERS);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          ref[w] = max(max(shared_top[w * 4], shared_top[w * 4 + 1]), max(shared_top[w * 4 + 2], shared_top[w * 4 + 3])) - 7;
+        if (tid == 0) {
+          refs[2 * (ui % C::NU)] = ref[0];
+          refs[2 * (ui % C::NU) + 1] = ref[1];
+        }
+        named_bar(5, C::LOADERS);  // before the next unit's maxima
+      }
+      auto load = [&](const uint8_t* base, const uint8_t* ex, int rf, int j) {
+        uint4 x[ITEMS];
+        uint32_t e[ITEMS];
+        const int valid = min(KB, u.len - j * KB);
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int it = i * C::LOADERS + tid, rr = it / ITEMS, ch = it % ITEMS;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          e[i] = 0;
+          if (rr < valid) {
+            const int64_t r = row_of(trow, j * KB + rr);
+            if (r >= 0) {
+              seq_ldg<16>(base + r * D + ch * 16, reinterpret_cast<uint32_t*>(&x[i]));
+              e[i] = __ldg(ex + r);
+            }
+          }
+        }
+        if (ok) ok = mbar_wait(&kv_empty[s], ph ^ 1u, status);
+        uint8_t* dst = tiles + s * C::TILEB;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+          const int it = i * C::LOADERS + tid, rr = it / ITEMS, ch = it % ITEMS;
+          uint32_t f2;
+          if constexpr (Half16<T>::kBF16) {
+            const float f = seq_pow(e[i]);
+            f2 = Half16<T>::pack2(f, f);
+          } else {
+            const float f = e[i] == 255 ? __uint_as_float(0x7FC00000u)
+                                        : seq_ex2(static_cast<float>(max(static_cast<int>(e[i]) - rf, -60) + 8));
+            f2 = Half16<T>::pack2(f, f);
+          }
+          uint32_t v[8];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t b = reinterpret_cast<const uint32_t*>(&x[i])[w];
+            v[2 * w] = seq_raw2<T>(__byte_perm(b, 0u, 0x1404));      // bytes 0, 1 at places 1, 3
+            v[2 * w + 1] = seq_raw2<T>(__byte_perm(b, 0u, 0x3424));  // bytes 2, 3
+          }
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            if constexpr (Half16<T>::kBF16) v[w] = seq_mul2<T>(v[w], 0x7B807B80u);
+            v[w] = seq_mul2<T>(v[w], f2);
+          }
+          // 16 elements: units 2 ch and 2 ch + 1 of the row
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int unit16 = 2 * ch + hh, bx = unit16 / (C::SWB / 16), jj = unit16 % (C::SWB / 16);
+            *reinterpret_cast<uint4*>(dst + bx * C::BOXB + whale_swz<C::SWB>(rr, jj)) =
+                make_uint4(v[4 * hh], v[4 * hh + 1], v[4 * hh + 2], v[4 * hh + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[s]);
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      };
+      const uint8_t *kb = static_cast<const uint8_t*>(K8), *vb = static_cast<const uint8_t*>(V8);
+      for (int j = u.j0; j < j1; ++j) {
+        if (j == u.j0) load(kb, a.k_exp, ref[0], j);
+        if (j + 1 < j1) load(kb, a.k_exp, ref[0], j + 1);
+        load(vb, a.v_exp, ref[1], j);
+      }
+      __syncwarp();
+      if (lane == 0) unit_done();
+      ++ui;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace wk

@@ -10,6 +10,7 @@
 #include "seq.cuh"
 #include "seq_cache.cuh"
 #include "seq_rows.cuh"
+#include "seq_tile.cuh"
 
 using namespace wk;
 
@@ -130,26 +131,89 @@ int64_t packed_rows(const SeqArgs& a) { return static_cast<int64_t>(a.max_q) * (
 int rows_nq(const SeqArgs& a) { return packed_rows(a) <= 8 ? 1 : 2; }
 int rows_pieces(int d, int nq) { return kSMs * seq_rows_occupancy(d, nq); }
 
+// Bytes of the notes and slots of `pieces` pieces of units of r rows.
+int64_t slot_bytes(int r, int d, int64_t pieces) {
+  return pieces * static_cast<int64_t>(sizeof(SeqNote)) + 2 * pieces * r * (d + 2) * 4;
+}
+
 // Bytes of partial results; none where no sequence has more than one key block.
 int64_t rows_ws(const SeqArgs& a, int d) {
   if (a.max_kv <= kRowsKB) return 0;
   const int nq = rows_nq(a);
-  return int64_t{4} * 2 * rows_pieces(d, nq) * 8 * nq * (d + 2);
+  return slot_bytes(8 * nq, d, rows_pieces(d, nq));
 }
 
 template <int D, typename T, int SRC, int NQ>
 wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* lse, float* ws, const SeqArgs& a,
                    cudaStream_t st) {
   const int64_t pieces = rows_pieces(D, NQ);
+  const bool cut = a.max_kv > kRowsKB;
   seq_rows_kernel<D, T, SRC, NQ><<<static_cast<unsigned>(pieces), SEQ_ROWS_THREADS, 0, st>>>(
-      static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse, ws, a, pieces);
+      static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse, cut ? ws : nullptr, a, pieces);
   const wk_status s = launch_status();
-  if (s != WK_OK || a.max_kv <= kRowsKB) return s;
-  return launch_dependent(seq_combine_kernel<8 * NQ, kRowsKB, D, SRC, T>, static_cast<unsigned>(pieces - 1),
-                          SEQ_COMBINE_THREADS, st, ws, static_cast<T*>(O), lse, a, pieces);
+  if (s != WK_OK || !cut) return s;
+  return launch_dependent(seq_combine_kernel<8 * NQ, 8 * NQ, D, T>, static_cast<unsigned>(pieces),
+                          SEQ_COMBINE_THREADS, st, ws, static_cast<T*>(O), lse, a.q_heads,
+                          static_cast<int32_t>(pieces));
 }
 
-int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : 0; }
+// ---- the tile kernel: any number of rows, 128 packed rows per tile (seq_tile.cuh)
+int64_t tile_ws(const SeqArgs& a, int d) { return a.max_kv <= 128 ? 0 : slot_bytes(128, d, kSMs); }
+
+// [tokens, heads, d] as a 3-D map (d, heads, tokens) with boxes (bw, 1, rows).
+template <typename T>
+bool map_tokens(const DevInfo* dv, CUtensorMap* m, const void* base, int d, int heads, int64_t tokens, int64_t stride,
+                int bw, int rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2};
+  const uint32_t box[3] = {static_cast<uint32_t>(bw), 1u, static_cast<uint32_t>(rows)};
+  return make_map(dv, m, tmap_dtype<T>(), 3, base, dims, strides, box,
+                  bw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// The rows of a 16-bit cache as a 2-D map (d, rows) with boxes of one page.
+template <typename T>
+bool map_pages(const DevInfo* dv, CUtensorMap* m, const void* base, int d, int64_t rows, int bw, int page) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(d) * 2};
+  const uint32_t box[2] = {static_cast<uint32_t>(bw), static_cast<uint32_t>(page)};
+  return make_map(dv, m, tmap_dtype<T>(), 2, base, dims, strides, box,
+                  bw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int D, typename T, int SRC>
+wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* V, void* O, float* lse, float* ws,
+                   const SeqArgs& a, cudaStream_t st) {
+  using C = StCfg<D, SRC>;
+  CUtensorMap mk{}, mv{};
+  if (SRC == SEQ_JAGGED && a.total_kv > 0) {
+    if (!map_tokens<T>(dv, &mk, K, D, a.kv_heads, a.total_kv, a.k_stride, C::BW, 128) ||
+        !map_tokens<T>(dv, &mv, V, D, a.kv_heads, a.total_kv, a.v_stride, C::BW, 128))
+      return WK_ERR_UNSUPPORTED;
+  } else if (SRC == SEQ_JAGGED) {  // no keys at all: the maps are not used
+    if (!map_tokens<T>(dv, &mk, Q, D, 1, 1, D, C::BW, 128)) return WK_ERR_UNSUPPORTED;
+    mv = mk;
+  } else if (SRC == SEQ_PAGED16) {
+    const int64_t rows = (static_cast<int64_t>(a.num_pages) * a.kv_heads) << a.page_shift;
+    if (rows > INT32_MAX || !map_pages<T>(dv, &mk, K, D, rows, C::BW, 1 << a.page_shift) ||
+        !map_pages<T>(dv, &mv, V, D, rows, C::BW, 1 << a.page_shift))
+      return WK_ERR_UNSUPPORTED;
+  }
+  auto fn = seq_tile_kernel<D, T, SRC>;
+  wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
+  if (s != WK_OK) return s;
+  const int64_t pieces = kSMs;
+  const bool cut = a.max_kv > 128;
+  fn<<<kSMs, C::THREADS, C::SMEM, st>>>(mk, mv, static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse,
+                                        cut ? ws : nullptr, a, pieces);
+  s = launch_status();
+  if (s != WK_OK || !cut) return s;
+  constexpr int CR = 16;
+  return launch_dependent(seq_combine_kernel<128, CR, D, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, st, ws,
+                          static_cast<T*>(O), lse, a.q_heads, static_cast<int32_t>(pieces));
+}
+
+int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : tile_ws(a, d); }
 
 constexpr int kWarps = 8;
 bool grid_of(int64_t warps, unsigned* grid) {
@@ -173,6 +237,7 @@ wk_status with_type(int d, wk_dtype t, F f) {
 }
 
 struct RunForward {
+  const DevInfo* dv;
   const void *Q, *K, *V;
   void* O;
   float* lse;
@@ -186,17 +251,15 @@ struct RunForward {
       return rows_nq(a) == 1
                  ? run_rows<D, T, SRC, 1>(Q, K, V, O, lse, ws, a, st)
                  : run_rows<D, T, SRC, 2>(Q, K, V, O, lse, ws, a, st);
-    unsigned grid;
-    if (!grid_of(static_cast<int64_t>(a.batch) * a.max_q * a.q_heads, &grid)) return WK_ERR_UNSUPPORTED;
-    xattn_forward_kernel<D, T, SRC><<<grid, 32 * kWarps, 0, st>>>(static_cast<const T*>(Q), K, V, static_cast<T*>(O),
-                                                                  lse, a);
-    return launch_status();
+    return run_tile<D, T, SRC>(dv, Q, K, V, O, lse, ws, a, st);
   }
   template <int D, typename T>
   wk_status operator()() const {
     return src == 0 ? run<D, T, 0>() : src == 1 ? run<D, T, 1>() : run<D, T, 2>();
   }
 };
+
+int64_t backward_ws(const wk_xattn_config& c) { return c.total_q * c.q_heads * 4; }
 
 struct RunBackward {
   const void *Q, *K, *V, *O, *dO;
@@ -268,7 +331,8 @@ wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* 
   if (!bytes) return WK_ERR_INVALID_ARG;
   const wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
-  *bytes = backward ? cfg->total_q * cfg->q_heads * 4 : forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
+  const int64_t forward = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
+  *bytes = backward ? std::max(forward, backward_ws(*cfg)) : forward;
   return WK_OK;
 }
 
@@ -296,7 +360,7 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cfg->d, cfg->dtype, RunForward{Q, K, V, O, lse, static_cast<float*>(workspace), a, 0, reinterpret_cast<cudaStream_t>(stream)});
+  return with_type(cfg->d, cfg->dtype, RunForward{dv, Q, K, V, O, lse, static_cast<float*>(workspace), a, 0, reinterpret_cast<cudaStream_t>(stream)});
 }
 
 wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V, const void* O,
@@ -432,7 +496,7 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   s = dev_info(&dv);
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
-  return with_type(cfg->d, cfg->dtype, RunForward{Q, cache->K, cache->V, O, lse, static_cast<float*>(workspace), a,
+  return with_type(cfg->d, cfg->dtype, RunForward{dv, Q, cache->K, cache->V, O, lse, static_cast<float*>(workspace), a,
                                                   cache->dtype == WK_E4M3 ? 2 : 1, reinterpret_cast<cudaStream_t>(stream)});
 }
 
