@@ -519,7 +519,7 @@ WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_wha
 
 typedef struct {
   int32_t batch;               /* sequences, >= 0 */
-  int32_t q_heads, kv_heads;   /* q_heads a multiple of kv_heads */
+  int32_t q_heads, kv_heads;   /* q_heads (at most 1024) a multiple of kv_heads, at most 64 times it */
   int32_t d;                   /* head width: 32, 64, 128 or 160 */
   int32_t max_q, max_kv;       /* most query rows / most keys of one sequence */
   int64_t total_q, total_kv;   /* rows of Q and O / of K and V (total_kv: not read by the cache calls) */

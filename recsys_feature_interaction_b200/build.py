@@ -19,7 +19,7 @@ SOURCES = {
     "wk_api.cu": COMMON + ["gemm_tc.cuh", "gemm_tc2.cuh", "lcb_tc.cuh", "fm_tc.cuh", "front_tc.cuh", "res_ln.cuh",
                            "res_ln_ring.cuh", "simt.cuh", "convert.cuh", "moe.cuh", "head.cuh", "whale.cuh",
                            "backward.cuh", "bw_tc.cuh"],
-    "wk_seq.cu": COMMON + ["seq_index.h", "seq_args.cuh", "seq.cuh", "seq_cache.cuh", "seq_rows.cuh", "seq_tile.cuh",
+    "wk_seq.cu": COMMON + ["seq_index.h", "seq_args.cuh", "seq_back.cuh", "seq_cache.cuh", "seq_rows.cuh", "seq_tile.cuh",
                            "whale.cuh"],
 }
 

@@ -27,6 +27,7 @@ struct SeqArgs {
   const int32_t* table;
   int32_t table_width, num_pages, page_shift, causal;
   const uint8_t *k_exp, *v_exp;
+  int32_t tile, block;  // backward: rows that stand and rows that go by, at a time
   unsigned* status;
 };
 
@@ -59,29 +60,51 @@ __device__ __forceinline__ float seq_ex2(float x) {
 struct SeqUnit {
   int32_t b, h, t;
   int32_t j0, j1, nb;   // nb: the unit's cost (1 for a unit without keys)
-  int32_t n, rows;      // query rows of the sequence; packed rows n * group
+  int32_t n, rows;      // query rows of the sequence; rows that stand (packed rows n * group, or keys)
   int32_t len;          // keys of the sequence
   int64_t q_begin, kv_begin;
 };
 
-// Cost of row tile t of a sequence.
-template <int R, int KB>
-__device__ __forceinline__ int seq_tile_cost(const SeqArgs& a, int n, int len, int group, int t) {
-  const int last = (min((t + 1) * R, n * group) - 1) / group;
-  const int nb = (seq_seen(len, n, last, a.causal) + KB - 1) / KB;
-  return nb > 1 ? nb : 1;
-}
+// What a kernel's units are: R stationary rows, key blocks (or, the other way round, row blocks) of
+// KB. The forward's: packed query rows stand, keys go by.
+template <int R_, int KB_, int SRC_>
+struct SeqPlan {
+  static constexpr int SRC = SRC_;
+  static __device__ __forceinline__ int R(const SeqArgs&) { return R_; }
+  static __device__ __forceinline__ int rows(int n, int len, int group) { return n * group; }
+  // blocks that tile t sees, at least 1
+  static __device__ __forceinline__ int cost(const SeqArgs& a, int n, int len, int group, int t) {
+    const int last = (min((t + 1) * R_, n * group) - 1) / group;
+    const int nb = (seq_seen(len, n, last, a.causal) + KB_ - 1) / KB_;
+    return nb > 1 ? nb : 1;
+  }
+  static __device__ __forceinline__ bool uniform(const SeqArgs& a) { return !a.causal; }
+};
 
-template <int R, int KB, int SRC>
+// The backward's: with SWAP keys stand and packed query rows go by. Tile and block sizes follow the
+// number of query heads that share a key head, so that both begin at a token: a.tile, a.block.
+template <bool SWAP>
+struct SeqPlanBack {
+  static constexpr int SRC = SEQ_JAGGED;
+  static __device__ __forceinline__ int R(const SeqArgs& a) { return a.tile; }
+  static __device__ __forceinline__ int rows(int n, int len, int group) { return SWAP ? len : n * group; }
+  static __device__ __forceinline__ int cost(const SeqArgs& a, int n, int len, int group, int t) {
+    const int nb = ((SWAP ? n * group : len) + a.block - 1) / a.block;
+    return nb > 1 ? nb : 1;
+  }
+  static __device__ __forceinline__ bool uniform(const SeqArgs&) { return true; }
+};
+
+template <class P>
 __device__ __forceinline__ int64_t seq_cost(const SeqArgs& a, int64_t b) {
-  const SeqSpan q = seq_queries(a, b), kv = seq_keys<SRC>(a, b);
+  const SeqSpan q = seq_queries(a, b), kv = seq_keys<P::SRC>(a, b);
   const int group = a.q_heads / a.kv_heads;
-  const int tiles = (q.len * group + R - 1) / R;
+  const int tiles = (P::rows(q.len, kv.len, group) + P::R(a) - 1) / P::R(a);
   int64_t s = 0;
-  if (a.causal) {
-    for (int t = 0; t < tiles; ++t) s += seq_tile_cost<R, KB>(a, q.len, kv.len, group, t);
+  if (!P::uniform(a)) {
+    for (int t = 0; t < tiles; ++t) s += P::cost(a, q.len, kv.len, group, t);
   } else if (tiles) {
-    s = static_cast<int64_t>(tiles) * seq_tile_cost<R, KB>(a, q.len, kv.len, group, 0);
+    s = static_cast<int64_t>(tiles) * P::cost(a, q.len, kv.len, group, 0);
   }
   return s * a.kv_heads;
 }
@@ -96,15 +119,15 @@ struct SeqPlace {
 
 // All threads call it (it synchronises the block); sh: NT / 32 + 4 values of shared memory. With
 // `tell`, spans out of range set the status word (block 0 only: it sees every sequence).
-template <int R, int KB, int SRC, int NT>
+template <class P, int NT>
 __device__ SeqPlace seq_place(const SeqArgs& a, int64_t piece, int64_t pieces, int64_t* sh, bool tell) {
   const int tid = threadIdx.x;
   const int64_t each = (a.batch + NT - 1) / NT;
   const int64_t b0 = min(static_cast<int64_t>(a.batch), tid * each), b1 = min(static_cast<int64_t>(a.batch), b0 + each);
   int64_t sum = 0;
   for (int64_t b = b0; b < b1; ++b) {
-    sum += seq_cost<R, KB, SRC>(a, b);
-    if (tell && (seq_queries(a, b).bad || seq_keys<SRC>(a, b).bad)) flag_error(a.status, kFlagBadShape);
+    sum += seq_cost<P>(a, b);
+    if (tell && (seq_queries(a, b).bad || seq_keys<P::SRC>(a, b).bad)) flag_error(a.status, kFlagBadShape);
   }
   // inclusive scan over the block
   const int lane = tid & 31, warp = tid >> 5;
@@ -133,7 +156,7 @@ __device__ SeqPlace seq_place(const SeqArgs& a, int64_t piece, int64_t pieces, i
   if (x - sum <= p.begin && p.begin < x) {  // exactly one thread's sequences hold it
     int64_t at = x - sum;
     for (int64_t b = b0; b < b1; ++b) {
-      const int64_t c = seq_cost<R, KB, SRC>(a, b);
+      const int64_t c = seq_cost<P>(a, b);
       if (p.begin < at + c) {
         sh[NT / 32] = b;
         sh[NT / 32 + 1] = p.begin - at;
@@ -152,7 +175,7 @@ __device__ SeqPlace seq_place(const SeqArgs& a, int64_t piece, int64_t pieces, i
 }
 
 // Walks the units of a piece.
-template <int R, int KB, int SRC>
+template <class P>
 struct SeqWalk {
   int64_t left;  // key blocks of the piece still to do
   SeqUnit u;
@@ -162,14 +185,14 @@ struct SeqWalk {
   __device__ __forceinline__ bool open(const SeqArgs& a) {
     for (; u.b < a.batch; ++u.b) {
       const SeqSpan q = seq_queries(a, u.b);
-      if (q.len == 0) continue;
-      const SeqSpan kv = seq_keys<SRC>(a, u.b);
+      const SeqSpan kv = seq_keys<P::SRC>(a, u.b);
+      u.rows = P::rows(q.len, kv.len, group);
+      if (u.rows == 0) continue;
       u.n = q.len;
-      u.rows = q.len * group;
       u.q_begin = q.begin;
       u.kv_begin = kv.begin;
       u.len = kv.len;
-      tiles = (u.rows + R - 1) / R;
+      tiles = (u.rows + P::R(a) - 1) / P::R(a);
       u.h = u.t = 0;
       return true;
     }
@@ -184,15 +207,15 @@ struct SeqWalk {
     u.b = p.b;
     open(a);
     int64_t into = p.into;
-    if (!a.causal) {  // every tile of the sequence costs the same
-      const int64_t c = seq_tile_cost<R, KB>(a, u.n, u.len, group, 0);
+    if (P::uniform(a)) {  // every tile of the sequence costs the same
+      const int64_t c = P::cost(a, u.n, u.len, group, 0);
       const int64_t skip = into / c;
       u.h = static_cast<int32_t>(skip / tiles);
       u.t = static_cast<int32_t>(skip % tiles);
       into -= skip * c;
     } else {
       for (;;) {
-        const int64_t c = seq_tile_cost<R, KB>(a, u.n, u.len, group, u.t);
+        const int64_t c = P::cost(a, u.n, u.len, group, u.t);
         if (into < c) break;
         into -= c;
         if (++u.t == tiles) {
@@ -207,7 +230,7 @@ struct SeqWalk {
   // The next unit of the piece in u; false at its end. Call start() first.
   __device__ __forceinline__ bool next(const SeqArgs& a) {
     if (left <= 0) return false;
-    u.nb = seq_tile_cost<R, KB>(a, u.n, u.len, group, u.t);
+    u.nb = P::cost(a, u.n, u.len, group, u.t);
     u.j1 = static_cast<int32_t>(min(static_cast<int64_t>(u.nb), u.j0 + left));
     left -= u.j1 - u.j0;
     return true;
@@ -233,7 +256,7 @@ struct SeqWalk {
 struct SeqNote {
   int32_t rows, r0;       // packed rows of the unit (0: the piece leaves none unfinished), the first one
   int32_t group, pieces;  // query heads per key head; pieces that the unit is spread over
-  int64_t q_begin;
+  int64_t begin;          // the sequence's first row of the tensor
   int32_t h, pad[3];
 };
 
@@ -256,17 +279,18 @@ struct SeqSlots {
 };
 
 // Every piece says what it leaves unfinished; by one thread, for a unit u of which the piece has
-// [j0, j1) with j0 == 0 and j1 < nb, or with none = true.
+// [j0, j1) with j0 == 0 and j1 < nb, or with none = true. begin: the sequence's first row of the
+// tensor that the unit's rows are of; tile: rows per unit.
 template <int R, int D>
-__device__ __forceinline__ void seq_leave_note(float* ws, int64_t piece, const SeqUnit& u, int group, int64_t per,
-                                               bool none) {
+__device__ __forceinline__ void seq_leave_note(float* ws, int64_t piece, const SeqUnit& u, int64_t begin, int tile,
+                                               int group, int64_t per, bool none) {
   SeqNote n;
-  n.rows = none ? 0 : min(R, u.rows - u.t * R);
-  n.r0 = u.t * R;
+  n.rows = none ? 0 : min(tile, u.rows - u.t * tile);
+  n.r0 = u.t * tile;
   n.group = group;
   // the unit's last key block lies nb - j1 blocks behind the piece's end
   n.pieces = none ? 0 : 1 + static_cast<int32_t>((u.nb - u.j1 + per - 1) / per);
-  n.q_begin = u.q_begin;
+  n.begin = begin;
   n.h = u.h;
   n.pad[0] = n.pad[1] = n.pad[2] = 0;
   *SeqSlots<R, D>::note(ws, piece) = n;
@@ -309,7 +333,7 @@ __global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no piece saw a key
     const int pr = n.r0 + r;
-    const int64_t row = (n.q_begin + pr / n.group) * q_heads + n.h * n.group + pr % n.group;
+    const int64_t row = (n.begin + pr / n.group) * q_heads + n.h * n.group + pr % n.group;
     *reinterpret_cast<uint4*>(O + row * D + d) =
         make_uint4(Half16<T>::pack2(o[0] * inv, o[1] * inv), Half16<T>::pack2(o[2] * inv, o[3] * inv),
                    Half16<T>::pack2(o[4] * inv, o[5] * inv), Half16<T>::pack2(o[6] * inv, o[7] * inv));

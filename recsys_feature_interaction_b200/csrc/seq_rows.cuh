@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
   __shared__ __align__(16) float sm_o[SEQ_ROWS_WARPS][R][PITCH];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const float scale_log2 = a.scale * 1.4426950408889634f;
-  const SeqPlace place = seq_place<R, C::KB, SRC, SEQ_ROWS_THREADS>(a, blockIdx.x, pieces, sh, blockIdx.x == 0);
+  const SeqPlace place = seq_place<SeqPlan<R, C::KB, SRC>, SEQ_ROWS_THREADS>(a, blockIdx.x, pieces, sh, blockIdx.x == 0);
   using S = SeqSlots<R, D>;
   bool left = false;  // a unit left unfinished
-  SeqWalk<R, C::KB, SRC> w;
+  SeqWalk<SeqPlan<R, C::KB, SRC>> w;
   w.start(a, place);
   for (; w.next(a); w.advance(a)) {
     const SeqUnit& u = w.u;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
     if (u.j0 == 0 && u.j1 < u.nb) {
       left = true;
-      if (threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, u, group, place.per, false);
+      if (threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, u, u.q_begin, R, group, place.per, false);
     }
     for (int i = threadIdx.x; i < rows * (D / 4); i += SEQ_ROWS_THREADS) {
       const int r = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     }
     __syncthreads();
   }
-  if (ws && !left && threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, w.u, w.group, place.per, true);
+  if (ws && !left && threadIdx.x == 0) seq_leave_note<R, D>(ws, blockIdx.x, w.u, 0, R, 1, place.per, true);
 }
 
 }  // namespace wk

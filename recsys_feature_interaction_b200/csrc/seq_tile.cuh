@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  const SeqPlace place = seq_place<R, KB, SRC, C::THREADS>(a, blockIdx.x, pieces, reinterpret_cast<int64_t*>(red), blockIdx.x == 0);
+  const SeqPlace place = seq_place<SeqPlan<R, KB, SRC>, C::THREADS>(a, blockIdx.x, pieces, reinterpret_cast<int64_t*>(red), blockIdx.x == 0);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   if (warp == 2) {
     // -------------------------------------------------------------- walker
     if (lane == 0) {
-      SeqWalk<R, KB, SRC> w;
+      SeqWalk<SeqPlan<R, KB, SRC>> w;
       w.start(a, place);
       bool left = false;  // a unit left unfinished
       for (;;) {
@@ -221,11 +221,11 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         if (!more) break;
         if (ws && w.u.j0 == 0 && w.u.j1 < w.u.nb) {
           left = true;
-          seq_leave_note<R, D>(ws, blockIdx.x, w.u, group, place.per, false);
+          seq_leave_note<R, D>(ws, blockIdx.x, w.u, w.u.q_begin, R, group, place.per, false);
         }
         w.advance(a);
       }
-      if (ws && !left) seq_leave_note<R, D>(ws, blockIdx.x, w.u, group, place.per, true);
+      if (ws && !left) seq_leave_note<R, D>(ws, blockIdx.x, w.u, 0, R, 1, place.per, true);
     }
   } else if (warp == 0 && SRC != SEQ_PAGED8) {
     // ------------------------------------------------------------ producer

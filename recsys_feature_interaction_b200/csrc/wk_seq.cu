@@ -1,13 +1,13 @@
 // wk_seq.cu -- the C ABI of attention over behaviour sequences (include/wukong.h): argument
 // checks, workspaces and launches of the jagged cross attention, its gradients and the paged cache.
-// The kernels are in seq.cuh.
+// The kernels are in seq_rows.cuh, seq_tile.cuh, seq_back.cuh and seq_cache.cuh.
 #include <algorithm>
 #include <cmath>
 
 #include "wukong.h"
 #include "common.cuh"
 #include "host.cuh"
-#include "seq.cuh"
+#include "seq_back.cuh"
 #include "seq_cache.cuh"
 #include "seq_rows.cuh"
 #include "seq_tile.cuh"
@@ -45,7 +45,8 @@ wk_status check_config(const wk_xattn_config* c) {
       c->max_kv < 0 || c->total_q < 0 || c->total_kv < 0 || c->total_q > kMaxRows || c->total_kv > kMaxRows ||
       c->max_kv > kMostRows || static_cast<int64_t>(c->max_q) * c->q_heads > kMostRows || !(c->scale >= 0.f) || !std::isfinite(c->scale))
     return WK_ERR_INVALID_ARG;
-  if (!seq_d_ok(c->d) || !type16(c->dtype) || c->q_heads > 1024) return WK_ERR_UNSUPPORTED;
+  if (!seq_d_ok(c->d) || !type16(c->dtype) || c->q_heads > 1024 || c->q_heads / c->kv_heads > 64)
+    return WK_ERR_UNSUPPORTED;
   const int64_t qs = stride_of(c->q_stride, c->q_heads, c->d), ks = stride_of(c->k_stride, c->kv_heads, c->d),
                 vs = stride_of(c->v_stride, c->kv_heads, c->d);
   const int64_t qd = static_cast<int64_t>(c->q_heads) * c->d, kd = static_cast<int64_t>(c->kv_heads) * c->d;
@@ -215,14 +216,6 @@ wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* 
 
 int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : tile_ws(a, d); }
 
-constexpr int kWarps = 8;
-bool grid_of(int64_t warps, unsigned* grid) {
-  const int64_t g = (warps + kWarps - 1) / kWarps;
-  if (g > INT32_MAX) return false;
-  *grid = static_cast<unsigned>(g);
-  return true;
-}
-
 // Calls f with the head width and the 16-bit type as compile-time values.
 template <typename F>
 wk_status with_type(int d, wk_dtype t, F f) {
@@ -259,30 +252,81 @@ struct RunForward {
   }
 };
 
-int64_t backward_ws(const wk_xattn_config& c) { return c.total_q * c.q_heads * 4; }
+// ---- the backward (seq_back.cuh): delta [total_q, q_heads], then the partial results, which the
+// two kernels use one after the other
+int64_t delta_bytes(const SeqArgs& a) { return (a.total_q * a.q_heads * 4 + 255) / 256 * 256; }
+int64_t backward_ws(const SeqArgs& a, int d) { return delta_bytes(a) + slot_bytes(128, 2 * d, kSMs); }
 
 struct RunBackward {
+  const DevInfo* dv;
   const void *Q, *K, *V, *O, *dO;
   const float* lse;
   void *dQ, *dK, *dV;
-  float* delta;
+  void* workspace;
   SeqArgs a;
   cudaStream_t st;
+
+  template <int D, typename T, bool DKV>
+  wk_status one(const CUtensorMap (&m)[4], float* delta, float* slots, void* G1, void* G2) const {
+    using C = SbCfg<D, DKV>;
+    SeqArgs x = a;
+    const int group = a.q_heads / a.kv_heads;
+    x.tile = DKV ? 128 : group * (128 / group);
+    x.block = DKV ? group * (64 / group) : 64;
+    auto fn = seq_back_kernel<D, T, DKV>;
+    wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
+    if (s != WK_OK) return s;
+    const int64_t pieces = kSMs;
+    fn<<<kSMs, C::THREADS, C::SMEM, st>>>(m[0], m[1], m[2], m[3], static_cast<const T*>(O), static_cast<const T*>(dO),
+                                          lse, delta, static_cast<T*>(G1), static_cast<T*>(G2), slots, x, pieces);
+    s = launch_status();
+    if (s != WK_OK) return s;
+    constexpr int CR = 16;
+    return launch_dependent(seq_sum_kernel<CR, D, C::NACC, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, st, slots,
+                            static_cast<T*>(G1), static_cast<T*>(G2), DKV ? a.kv_heads : a.q_heads,
+                            static_cast<int32_t>(pieces));
+  }
+
   template <int D, typename T>
   wk_status operator()() const {
-    unsigned g0, g1, g2;
-    const int64_t rows = a.total_q * a.q_heads;
-    if (!grid_of(rows, &g0) || !grid_of(static_cast<int64_t>(a.batch) * a.max_q * a.q_heads, &g1) ||
-        !grid_of(a.total_kv * a.kv_heads, &g2))
+    constexpr int BW = SbCfg<D, false>::BW;
+    const int group = a.q_heads / a.kv_heads;
+    // without rows (or without keys) the tensors may be NULL; their maps are then not used
+    const void* any = a.total_q > 0 ? Q : K;
+    auto map = [&](CUtensorMap* m, const void* p, int heads, int64_t tokens, int64_t stride, int box_heads, int box_tokens) {
+      const uint64_t dims[3] = {D, static_cast<uint64_t>(heads), static_cast<uint64_t>(std::max<int64_t>(tokens, 1))};
+      const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(stride) * 2};
+      const uint32_t box[3] = {BW, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_tokens)};
+      return make_map(dv, m, tmap_dtype<T>(), 3, tokens > 0 ? p : any, dims, strides, box,
+                      BW == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    const int64_t od = static_cast<int64_t>(a.q_heads) * D;
+    CUtensorMap q[4], k[4];  // the maps of DQ and of DKV
+    if (!map(&q[0], Q, a.q_heads, a.total_q, a.q_stride, group, 128 / group) ||
+        !map(&q[1], dO, a.q_heads, a.total_q, od, group, 128 / group) ||
+        !map(&q[2], K, a.kv_heads, a.total_kv, a.k_stride, 1, 64) ||
+        !map(&q[3], V, a.kv_heads, a.total_kv, a.v_stride, 1, 64) ||
+        !map(&k[0], K, a.kv_heads, a.total_kv, a.k_stride, 1, 128) ||
+        !map(&k[1], V, a.kv_heads, a.total_kv, a.v_stride, 1, 128) ||
+        !map(&k[2], Q, a.q_heads, a.total_q, a.q_stride, group, 64 / group) ||
+        !map(&k[3], dO, a.q_heads, a.total_q, od, group, 64 / group))
       return WK_ERR_UNSUPPORTED;
-    const T *q = static_cast<const T*>(Q), *k = static_cast<const T*>(K), *v = static_cast<const T*>(V),
-            *go = static_cast<const T*>(dO);
-    if (g0) xattn_delta_kernel<D, T><<<g0, 32 * kWarps, 0, st>>>(static_cast<const T*>(O), go, delta, rows);
-    if (g1) xattn_dq_kernel<D, T><<<g1, 32 * kWarps, 0, st>>>(q, k, v, go, lse, delta, static_cast<T*>(dQ), a);
-    if (g2)
-      xattn_dkv_kernel<D, T>
-          <<<g2, 32 * kWarps, 0, st>>>(q, k, v, go, lse, delta, static_cast<T*>(dK), static_cast<T*>(dV), a);
-    return launch_status();
+    float* delta = static_cast<float*>(workspace);
+    float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes(a));
+    if (a.total_q > 0) {
+      const wk_status s = one<D, T, false>(q, delta, slots, dQ, nullptr);
+      if (s != WK_OK) return s;
+    }
+    if (a.total_kv > 0) {
+      const wk_status s = one<D, T, true>(k, delta, slots, dK, dV);
+      if (s != WK_OK) return s;
+      if (a.kv_lens) {
+        seq_zero_padding_kernel<T><<<dim3(static_cast<unsigned>(a.batch), 2), 256, 0, st>>>(
+            static_cast<T*>(dK), static_cast<T*>(dV), static_cast<int64_t>(a.kv_heads) * D, a);
+        return launch_status();
+      }
+    }
+    return WK_OK;
   }
 };
 
@@ -332,7 +376,7 @@ wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* 
   const wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
   const int64_t forward = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
-  *bytes = backward ? std::max(forward, backward_ws(*cfg)) : forward;
+  *bytes = backward ? std::max(forward, backward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d)) : forward;
   return WK_OK;
 }
 
@@ -403,8 +447,7 @@ wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const voi
   if (s != WK_OK) return s;
   a.status = dv->standalone_status;
   return with_type(cfg->d, cfg->dtype,
-                   RunBackward{Q, K, V, O, dO, lse, dQ, dK, dV, static_cast<float*>(workspace), a,
-                               reinterpret_cast<cudaStream_t>(stream)});
+                   RunBackward{dv, Q, K, V, O, dO, lse, dQ, dK, dV, workspace, a, reinterpret_cast<cudaStream_t>(stream)});
 }
 
 wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, int64_t k_stride, int64_t v_stride,
