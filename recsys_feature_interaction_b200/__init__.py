@@ -613,14 +613,21 @@ def wk_whale_fusion_ffn(Hw, A, weights, Hf, rows, d, h, dtype, eps=0.0, stream=N
 
 # ------------------------------------- attention over behaviour sequences, paged cache
 
+# These calls are made once per request or layer and some run for a few microseconds, so the checks
+# below compare dtype objects and integers only.
+_torch = None
+
+
 def _int32(t, name, *shape):
-    """Device int32 data of the given leading sizes (None: any), dense; its address."""
+    """Address of dense int32 data of the given sizes (None: any size)."""
     if t is None:
         return None
-    if str(t.dtype) != "torch.int32" or t.dim() != len(shape) or not t.is_contiguous():
+    have = t.shape
+    if t.dtype is not _torch.int32 or len(have) != len(shape) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of %d dimensions" % (name, len(shape)))
-    if any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    for x, want in zip(have, shape):
+        if want is not None and x != want:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(have), shape))
     return t.data_ptr()
 
 
@@ -629,28 +636,53 @@ def _tokens(t, name):
     if t.dim() != 3:
         raise ValueError("%s must be [tokens, heads, d]" % name)
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError("the heads of a token of %s must be dense" % name)
-    return n, h, d, (t.stride(0) if n > 1 else h * d)
+    return n, h, d, (s0 if n > 1 else h * d)
 
 
 def _dense(t, name, shape, dtype):
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
     return t.data_ptr()
 
 
+def _code16(dtype):
+    """The library's code of a 16-bit type; other types are refused by the library."""
+    return WK_BF16 if dtype is _torch.bfloat16 else WK_F16 if dtype is _torch.float16 else _dtype_code(dtype)
+
+
 def _call(name, args, stream, tensors):
     """Calls lib().<name>(*args, stream) with the tensors' device as the current one."""
-    import torch
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("%s takes tensors of one CUDA device, got %s"
+                             % (name, sorted({str(t.device) for t in tensors if t is not None})))
+    if stream is None:
+        stream = _torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if _torch._C._cuda_getDevice() == dev:
+        status = getattr(_lib, name)(*args, stream)
+    else:
+        with _torch.cuda.device(dev):
+            status = getattr(_lib, name)(*args, stream)
+    if status != WK_OK:
+        raise WkError(status, name)
 
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1 or next(iter(devs)).type != "cuda":
-        raise ValueError("%s takes tensors of one CUDA device, got %s" % (name, sorted(map(str, devs))))
-    with torch.cuda.device(next(iter(devs))):
-        _check(getattr(lib(), name)(*args, _stream(stream, tensors[0])), name)
+
+def _ready():
+    """Loads torch and the library on the first of these calls."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        lib()
+        _torch = torch
 
 
 def _scratch(workspace):
@@ -658,21 +690,22 @@ def _scratch(workspace):
         return None, 0
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    return (workspace.data_ptr() if workspace.numel() else None), workspace.numel() * workspace.element_size()
+    n = workspace.numel()
+    return (workspace.data_ptr() if n else None), n * workspace.element_size()
 
 
 def _xattn_config(Q, K, V, batch, max_q, max_kv, scale):
     tq, hq, d, qs = _tokens(Q, "Q")
     tk, hk, dk, ks = _tokens(K, "K")
     tv, hv, dv, vs = _tokens(V, "V")
-    if dk != d or dv != d or hv != hk or tv != tk or K.dtype != Q.dtype or V.dtype != Q.dtype:
+    if dk != d or dv != d or hv != hk or tv != tk or K.dtype is not Q.dtype or V.dtype is not Q.dtype:
         raise ValueError("Q, K and V disagree: %s, %s, %s" % (tuple(Q.shape), tuple(K.shape), tuple(V.shape)))
-    return WkXattnConfig(int(batch), hq, hk, d, int(max_q), int(max_kv), tq, tk, qs, ks, vs, _dtype_code(Q.dtype),
-                         float(scale))
+    return WkXattnConfig(batch, hq, hk, d, max_q, max_kv, tq, tk, qs, ks, vs, _code16(Q.dtype), scale)
 
 
 def wk_xattn_workspace(Q, K, batch, max_q, max_kv, backward=False):
-    """Bytes of device workspace that the forward (or the backward) of these tensors needs."""
+    """Bytes of device workspace that the forward of these tensors needs (backward=True: a whole training step)."""
+    _ready()
     c = _xattn_config(Q, K, K, batch, max_q, max_kv, 0.0)
     n = ctypes.c_int64()
     _check(lib().wk_xattn_workspace(ctypes.byref(c), int(bool(backward)), ctypes.byref(n)), "wk_xattn_workspace")
@@ -684,25 +717,23 @@ def wk_xattn_forward(Q, K, V, O, q_off, kv_off, max_q, max_kv, kv_lens=None, lse
     """O[i] = softmax(scale * Q[i] K^T) V of jagged sequences: Q, O [tokens, q_heads, d], K, V [tokens, kv_heads, d]
     (tokens may be strided), q_off, kv_off int32 boundaries [batch + 1], kv_lens int32 [batch] or None, lse fp32
     [tokens, q_heads] or None. workspace: a tensor of at least wk_xattn_workspace bytes, this call's own while it runs."""
-    import torch
-
+    _ready()
     batch = q_off.shape[0] - 1
     c = _xattn_config(Q, K, V, batch, max_q, max_kv, scale)
-    args = [ctypes.byref(c), _addr(Q), _addr(K), _addr(V), _int32(q_off, "q_off", None),
+    args = [ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _int32(q_off, "q_off", None),
             _int32(kv_off, "kv_off", batch + 1), _int32(kv_lens, "kv_lens", batch), _dense(O, "O", Q.shape, Q.dtype),
-            _dense(lse, "lse", Q.shape[:2], torch.float32), *_scratch(workspace)]
-    _call("wk_xattn_forward", args, stream, [Q, K, V, O, q_off, kv_off, kv_lens, lse, workspace])
+            _dense(lse, "lse", Q.shape[:2], _torch.float32), *_scratch(workspace)]
+    _call("wk_xattn_forward", args, stream, (Q, K, V, O, q_off, kv_off, kv_lens, lse, workspace))
 
 
 def wk_xattn_backward(Q, K, V, O, lse, dO, dQ, dK, dV, q_off, kv_off, max_q, max_kv, kv_lens=None, scale=0.0,
                       workspace=None, stream=None):
     """Gradients of sum(O * dO) for the forward of the same arguments: dQ, dK, dV (dense) are overwritten."""
-    import torch
-
+    _ready()
     batch = q_off.shape[0] - 1
     c = _xattn_config(Q, K, V, batch, max_q, max_kv, scale)
-    args = [ctypes.byref(c), _addr(Q), _addr(K), _addr(V), _dense(O, "O", Q.shape, Q.dtype),
-            _dense(lse, "lse", Q.shape[:2], torch.float32), _dense(dO, "dO", Q.shape, Q.dtype),
+    args = [ctypes.byref(c), Q.data_ptr(), K.data_ptr(), V.data_ptr(), _dense(O, "O", Q.shape, Q.dtype),
+            _dense(lse, "lse", Q.shape[:2], _torch.float32), _dense(dO, "dO", Q.shape, Q.dtype),
             _int32(q_off, "q_off", None), _int32(kv_off, "kv_off", batch + 1), _int32(kv_lens, "kv_lens", batch),
             _dense(dQ, "dQ", Q.shape, Q.dtype), _dense(dK, "dK", K.shape, Q.dtype), _dense(dV, "dV", V.shape, Q.dtype),
             *_scratch(workspace)]
@@ -710,21 +741,26 @@ def wk_xattn_backward(Q, K, V, O, lse, dO, dQ, dK, dV, q_off, kv_off, max_q, max
 
 
 def _cache(cache):
-    """cache: mapping with K, V [pages, kv_heads, page_size, d] (16-bit, or 8-bit: float8_e4m3fn or uint8) and, with
-    8 bits, K_exp, V_exp uint8 [pages, kv_heads, page_size]."""
+    """(WkCache, its tensors). cache: mapping with K, V [pages, kv_heads, page_size, d] (16-bit, or 8-bit:
+    float8_e4m3fn or uint8) and, with 8 bits, K_exp, V_exp uint8 [pages, kv_heads, page_size]."""
+    _ready()
     K, V, ke, ve = cache["K"], cache["V"], cache.get("K_exp"), cache.get("V_exp")
-    if K.dim() != 4 or K.shape != V.shape or K.dtype != V.dtype or not K.is_contiguous() or not V.is_contiguous():
+    shape, dtype = K.shape, K.dtype
+    if len(shape) != 4 or V.shape != shape or V.dtype is not dtype or not K.is_contiguous() or not V.is_contiguous():
         raise ValueError("a cache's K and V must be contiguous [pages, kv_heads, page_size, d] tensors of one type")
-    eight = K.element_size() == 1
-    if eight and str(K.dtype) not in ("torch.float8_e4m3fn", "torch.uint8"):
+    eight = dtype is _torch.float8_e4m3fn or dtype is _torch.uint8
+    if not eight and K.element_size() == 1:
         raise ValueError("an 8-bit cache holds e4m3 values")
-    for t in (ke, ve):
-        if eight != (t is not None):
-            raise ValueError("K_exp and V_exp belong to 8-bit caches, and to those only")
-        if t is not None and (t.shape != K.shape[:3] or str(t.dtype) != "torch.uint8" or not t.is_contiguous()):
-            raise ValueError("K_exp and V_exp must be contiguous uint8 [pages, kv_heads, page_size]")
-    return WkCache(_addr(K), _addr(V), _addr(ke), _addr(ve), K.shape[0], K.shape[2], K.shape[1], K.shape[3],
-                   WK_E4M3 if eight else _dtype_code(K.dtype)), [K, V, ke, ve]
+    if (ke is not None) != eight or (ve is not None) != eight:
+        raise ValueError("K_exp and V_exp belong to 8-bit caches, and to those only")
+    pages, heads, page, d = shape
+    if eight:
+        for t in (ke, ve):
+            if t.dtype is not _torch.uint8 or t.shape != shape[:3] or not t.is_contiguous():
+                raise ValueError("K_exp and V_exp must be contiguous uint8 [pages, kv_heads, page_size]")
+        return (WkCache(K.data_ptr(), V.data_ptr(), ke.data_ptr(), ve.data_ptr(), pages, page, heads, d, WK_E4M3),
+                (K, V, ke, ve))
+    return WkCache(K.data_ptr(), V.data_ptr(), None, None, pages, page, heads, d, _code16(dtype)), (K, V)
 
 
 def wk_cache_write(cache, K, V, new_off, table, kv_lens, max_new, stream=None):
@@ -733,31 +769,30 @@ def wk_cache_write(cache, K, V, new_off, table, kv_lens, max_new, stream=None):
     c, held = _cache(cache)
     n, h, d, ks = _tokens(K, "K")
     nv, hv, dv, vs = _tokens(V, "V")
-    if (n, h, d) != (nv, hv, dv) or (h, d) != (c.kv_heads, c.d) or V.dtype != K.dtype:
+    if (n, h, d) != (nv, hv, dv) or (h, d) != (c.kv_heads, c.d) or V.dtype is not K.dtype:
         raise ValueError("K, V and the cache disagree")
     batch = new_off.shape[0] - 1
-    args = [ctypes.byref(c), _addr(K), _addr(V), ks, vs, _dtype_code(K.dtype), _int32(new_off, "new_off", None),
+    args = [ctypes.byref(c), K.data_ptr(), V.data_ptr(), ks, vs, _code16(K.dtype), _int32(new_off, "new_off", None),
             _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch), batch, n,
             int(max_new)]
-    _call("wk_cache_write", args, stream, [K, V, new_off, table, kv_lens] + held)
+    _call("wk_cache_write", args, stream, (K, V, new_off, table, kv_lens, *held))
 
 
 def wk_cache_read(cache, table, kv_lens, out_off, K, V, max_kv, stream=None):
     """Reads the cached sequences into rows out_off[b] .. out_off[b] + kv_lens[b] of K, V [tokens, kv_heads, d]."""
     c, held = _cache(cache)
     batch = out_off.shape[0] - 1
-    if K.dim() != 3 or tuple(K.shape[1:]) != (c.kv_heads, c.d):
+    if K.dim() != 3 or K.shape[1:] != held[0].shape[1::2]:
         raise ValueError("K must be [tokens, kv_heads, d] of the cache")
     args = [ctypes.byref(c), _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
             _int32(out_off, "out_off", None), _dense(K, "K", K.shape, K.dtype), _dense(V, "V", K.shape, K.dtype),
-            _dtype_code(K.dtype), batch, K.shape[0], int(max_kv)]
-    _call("wk_cache_read", args, stream, [K, V, out_off, table, kv_lens] + held)
+            _code16(K.dtype), batch, K.shape[0], int(max_kv)]
+    _call("wk_cache_read", args, stream, (K, V, out_off, table, kv_lens, *held))
 
 
 def _cache_config(c, Q, batch, max_q, max_kv, scale):
     tq, hq, d, qs = _tokens(Q, "Q")
-    return WkXattnConfig(int(batch), hq, c.kv_heads, d, int(max_q), int(max_kv), tq, 0, qs, 0, 0, _dtype_code(Q.dtype),
-                         float(scale))
+    return WkXattnConfig(batch, hq, c.kv_heads, d, max_q, max_kv, tq, 0, qs, 0, 0, _code16(Q.dtype), scale)
 
 
 def wk_cache_attention_workspace(cache, Q, batch, max_q, max_kv):
@@ -774,14 +809,11 @@ def wk_cache_attention(cache, Q, O, q_off, table, kv_lens, max_q, max_kv, causal
                        workspace=None, stream=None):
     """Attention of each sequence's rows of Q (its newest tokens when causal, candidates otherwise) over its cached
     keys. Q, O [tokens, q_heads, d]; table [batch, width], kv_lens [batch], q_off [batch + 1] int32."""
-    import torch
-
     c, held = _cache(cache)
     batch = q_off.shape[0] - 1
     cfg = _cache_config(c, Q, batch, max_q, max_kv, scale)
-    ws, nws = _scratch(workspace)
-    args = [ctypes.byref(c), ctypes.byref(cfg), _addr(Q), _int32(q_off, "q_off", None),
+    args = [ctypes.byref(c), ctypes.byref(cfg), Q.data_ptr(), _int32(q_off, "q_off", None),
             _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
-            int(bool(causal)), _dense(O, "O", Q.shape, Q.dtype), _dense(lse, "lse", Q.shape[:2], torch.float32),
+            1 if causal else 0, _dense(O, "O", Q.shape, Q.dtype), _dense(lse, "lse", Q.shape[:2], _torch.float32),
             *_scratch(workspace)]
-    _call("wk_cache_attention", args, stream, [Q, O, q_off, table, kv_lens, lse, workspace] + held)
+    _call("wk_cache_attention", args, stream, (Q, O, q_off, table, kv_lens, lse, workspace, *held))

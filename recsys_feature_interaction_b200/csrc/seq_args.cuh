@@ -9,7 +9,8 @@
 // however few its rows, and which block does what depends on the lengths alone. A unit that a cut
 // goes through is finished by the combine kernel from fp32 partial results: piece c leaves those of
 // the unit it enters in the middle in slot 2c, those of the unit it leaves unfinished in slot 2c + 1,
-// and a note about the latter.
+// and a note about the latter. Where sequences are so short that a cut would save less than joining
+// the parts costs, the line is made of whole units instead (uncut).
 #pragma once
 
 #include "common.cuh"
@@ -27,7 +28,8 @@ struct SeqArgs {
   const int32_t* table;
   int32_t table_width, num_pages, page_shift, causal;
   const uint8_t *k_exp, *v_exp;
-  int32_t tile, block;  // backward: rows that stand and rows that go by, at a time
+  int32_t tile, block;  // rows that stand at a time (whole tokens), and rows that go by (backward)
+  int32_t uncut;        // units are not cut: a piece is a number of whole units
   unsigned* status;
 };
 
@@ -66,15 +68,15 @@ struct SeqUnit {
 };
 
 // What a kernel's units are: R stationary rows, key blocks (or, the other way round, row blocks) of
-// KB. The forward's: packed query rows stand, keys go by.
+// KB. The forward's: packed query rows stand, keys go by. R_ = 0: a.tile rows.
 template <int R_, int KB_, int SRC_>
 struct SeqPlan {
   static constexpr int SRC = SRC_;
-  static __device__ __forceinline__ int R(const SeqArgs&) { return R_; }
+  static __device__ __forceinline__ int R(const SeqArgs& a) { return R_ ? R_ : a.tile; }
   static __device__ __forceinline__ int rows(int n, int len, int group) { return n * group; }
   // blocks that tile t sees, at least 1
   static __device__ __forceinline__ int cost(const SeqArgs& a, int n, int len, int group, int t) {
-    const int last = (min((t + 1) * R_, n * group) - 1) / group;
+    const int last = (min((t + 1) * R(a), n * group) - 1) / group;
     const int nb = (seq_seen(len, n, last, a.causal) + KB_ - 1) / KB_;
     return nb > 1 ? nb : 1;
   }
@@ -101,7 +103,9 @@ __device__ __forceinline__ int64_t seq_cost(const SeqArgs& a, int64_t b) {
   const int group = a.q_heads / a.kv_heads;
   const int tiles = (P::rows(q.len, kv.len, group) + P::R(a) - 1) / P::R(a);
   int64_t s = 0;
-  if (!P::uniform(a)) {
+  if (a.uncut) {
+    s = tiles;
+  } else if (!P::uniform(a)) {
     for (int t = 0; t < tiles; ++t) s += P::cost(a, q.len, kv.len, group, t);
   } else if (tiles) {
     s = static_cast<int64_t>(tiles) * P::cost(a, q.len, kv.len, group, 0);
@@ -207,8 +211,8 @@ struct SeqWalk {
     u.b = p.b;
     open(a);
     int64_t into = p.into;
-    if (P::uniform(a)) {  // every tile of the sequence costs the same
-      const int64_t c = P::cost(a, u.n, u.len, group, 0);
+    if (a.uncut || P::uniform(a)) {  // every tile of the sequence costs the same
+      const int64_t c = a.uncut ? 1 : P::cost(a, u.n, u.len, group, 0);
       const int64_t skip = into / c;
       u.h = static_cast<int32_t>(skip / tiles);
       u.t = static_cast<int32_t>(skip % tiles);
@@ -231,6 +235,11 @@ struct SeqWalk {
   __device__ __forceinline__ bool next(const SeqArgs& a) {
     if (left <= 0) return false;
     u.nb = P::cost(a, u.n, u.len, group, u.t);
+    if (a.uncut) {
+      u.j1 = u.nb;
+      --left;
+      return true;
+    }
     u.j1 = static_cast<int32_t>(min(static_cast<int64_t>(u.nb), u.j0 + left));
     left -= u.j1 - u.j0;
     return true;

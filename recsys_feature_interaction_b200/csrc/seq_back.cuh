@@ -124,6 +124,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     }
     fence_mbar_init();
   }
+  // nothing of the kernels before is read above, and no TMEM is taken that they may still need
+  cudaGridDependencySynchronize();
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -163,14 +165,14 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         mbar_arrive(&u_full[s]);
         ++ui;
         if (!more) break;
-        if (w.u.j0 == 0 && w.u.j1 < w.u.nb) {
+        if (ws && w.u.j0 == 0 && w.u.j1 < w.u.nb) {
           left = true;
           seq_leave_note<128, C::NACC * D>(ws, blockIdx.x, w.u, DKV ? w.u.kv_begin : w.u.q_begin, a.tile,
                                            DKV ? 1 : group, place.per, false);
         }
         w.advance(a);
       }
-      if (!left) seq_leave_note<128, C::NACC * D>(ws, blockIdx.x, w.u, 0, a.tile, 1, place.per, true);
+      if (ws && !left) seq_leave_note<128, C::NACC * D>(ws, blockIdx.x, w.u, 0, a.tile, 1, place.per, true);
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -552,6 +554,7 @@ __global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
 // Zeros in the rows between a sequence's last key and the next sequence (padded batches).
 template <typename T>
 __global__ void seq_zero_padding_kernel(T* __restrict__ dK, T* __restrict__ dV, int64_t row_elems, SeqArgs a) {
+  cudaGridDependencySynchronize();
   const SeqSpan kv = seq_keys<SEQ_JAGGED>(a, blockIdx.x);
   const int64_t at = (kv.begin + kv.len) * row_elems / 8;
   const int64_t n = static_cast<int64_t>(kv.room - kv.len) * row_elems / 8;

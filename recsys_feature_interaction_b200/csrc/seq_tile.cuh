@@ -1,8 +1,8 @@
 // seq_tile.cuh -- attention of more than 16 packed query rows per (sequence, key head) on the
 // 5th-generation tensor cores, over jagged tensors or a cache.
 //
-// A block holds 128 packed query rows (SeqUnit) and walks 128-key blocks: S = Q K^T with Q in TMEM
-// and the K tile K-major in shared memory, softmax weights from TMEM by two warps per lane quarter,
+// A block holds up to 128 packed query rows (whole tokens of the query heads that share a key head)
+// and walks 128-key blocks: S = Q K^T from shared memory, softmax weights from TMEM by two warps per lane quarter,
 // P written over S's columns, O += P V with the V tile MN-major. S is double-buffered, S of the
 // next block is issued before P V of this one, K and V tiles arrive in one ring in the order in
 // which the products use them (K0, K1, V0, K2, V1, ..).
@@ -63,15 +63,37 @@ __device__ __forceinline__ float seq_max2(float a, float b) {
   return r;
 }
 
-// whale_ex2_poly with a floor whose result rounds to 0 in both 16-bit types, so that a masked score
-// (-inf) gets a weight of exactly 0: at x = -126.9997 the integer part is -127 and the polynomial
-// just above 1, so that adding -127 to its exponent leaves a subnormal below 2^-139.
-__device__ __forceinline__ float seq_ex2_poly(float x) {
-  x = fmaxf(x, -126.9997f);
-  const float t = x + 12582912.f;
-  const float f = x - (t - 12582912.f);
-  const float p = fmaf(fmaf(fmaf(0.05517158f, f, 0.24261111f), f, 0.69326103f), f, 0.99992806f);
-  return __uint_as_float(__float_as_uint(p) + (__float_as_uint(t) << 23));
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 seq_fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)), "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 seq_add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
+// 2^x of two values on the FMA pipe (see whale_ex2_poly), with a floor whose result rounds to 0 in
+// both 16-bit types, so that a masked score (-inf) gets a weight of exactly 0: at x = -126.9997 the
+// integer part is -127 and the polynomial just above 1, so that adding -127 to its exponent leaves
+// a subnormal below 2^-139.
+__device__ __forceinline__ float2 seq_ex2_poly(float2 x) {
+  const float2 big = make_float2(12582912.f, 12582912.f), nbig = make_float2(-12582912.f, -12582912.f);
+  x = make_float2(fmaxf(x.x, -126.9997f), fmaxf(x.y, -126.9997f));
+  const float2 t = seq_add2(x, big);
+  const float2 j = seq_add2(t, nbig);
+  const float2 f = seq_add2(x, make_float2(-j.x, -j.y));
+  float2 p = seq_fma2(make_float2(0.05517158f, 0.05517158f), f, make_float2(0.24261111f, 0.24261111f));
+  p = seq_fma2(p, f, make_float2(0.69326103f, 0.69326103f));
+  p = seq_fma2(p, f, make_float2(0.99992806f, 0.99992806f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 template <int N>
@@ -106,17 +128,18 @@ struct StCfg {
   static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
   static constexpr int REDB = 4 * R * 4;                 // softmax pair exchange [2 parities][2 halves][R]
   static constexpr int FIXED = BARB + UNITB + REDB;
-  static constexpr int STAGES_RAW = (LIMIT - FIXED) / TILEB;
+  static constexpr int QBUF = D <= 128 ? 2 : 1;          // Q tiles in flight: d = 160 has no room for two
+  static constexpr int STAGES_RAW = (LIMIT - FIXED - QBUF * TILEB) / TILEB;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   // more than half an SM's shared memory: one block per SM, whose 512 TMEM columns are its own
-  static constexpr int SMEM = FIXED + STAGES * TILEB > 120 * 1024 ? FIXED + STAGES * TILEB : 120 * 1024;
-  // TMEM: S0, S1 [0, 256) (P over their first 64 columns), O [256, 256 + D), Q behind it
+  static constexpr int RAW = FIXED + (QBUF + STAGES) * TILEB;
+  static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
+  // TMEM: S0, S1 [0, 256) (P over their first 64 columns), O [256, 256 + D)
   static constexpr int OCOL = 2 * KB;
-  static constexpr int QCOL = OCOL + D;
   static constexpr int THREADS = SRC == SEQ_PAGED8 ? 512 : 384;
   static constexpr int LOADERS = 128;
-  static_assert(QCOL + D / 2 <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
-  static_assert((2 * STAGES + 9 + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
+  static_assert(OCOL + D <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
+  static_assert((2 * STAGES + 8 + 2 * QBUF + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
 };
 
 // Key blocks [j0, j1) of a unit that hold keys (a unit without keys has a cost, but no block).
@@ -127,8 +150,8 @@ __device__ __forceinline__ int seq_real_end(const SeqArgs& a, const SeqUnit& u, 
 
 template <int D, typename T, int SRC>
 __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
-    seq_tile_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const T* __restrict__ Q, const void* __restrict__ K8, const void* __restrict__ V8,
+    seq_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const void* __restrict__ K8, const void* __restrict__ V8,
                     T* __restrict__ O, float* __restrict__ lse, float* __restrict__ ws, SeqArgs a, int64_t pieces) {
   using C = StCfg<D, SRC>;
   constexpr int R = C::R, KB = C::KB;
@@ -137,17 +160,19 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     if (threadIdx.x == 0) flag_error(a.status, kFlagBadShape);
     return;
   }
-  uint8_t* tiles = smem_raw;
+  uint8_t* sQ = smem_raw;                              // [QBUF]
+  uint8_t* tiles = sQ + C::QBUF * C::TILEB;            // [STAGES]
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::TILEB);
   uint64_t* kv_full = bars;                  // [STAGES] tile landed
   uint64_t* kv_empty = bars + C::STAGES;     // [STAGES] its product has read it
   uint64_t* s_full = bars + 2 * C::STAGES;   // [2] S in TMEM
   uint64_t* p_full = s_full + 2;             // [2] P in TMEM
   uint64_t* p_empty = s_full + 4;            // [2] P V has read it (so O holds that block)
-  uint64_t* q_full = s_full + 6;             // the unit's Q rows are in TMEM
-  uint64_t* o_empty = s_full + 7;            // O read by the softmax warps (per unit)
-  uint64_t* fin = s_full + 8;
-  uint64_t* u_full = s_full + 9;             // [NU] unit handed over
+  uint64_t* o_empty = s_full + 6;            // O read by the softmax warps (per unit)
+  uint64_t* fin = s_full + 7;
+  uint64_t* q_full = s_full + 8;             // [QBUF] the unit's Q rows landed
+  uint64_t* q_empty = q_full + C::QBUF;      // [QBUF] its last S has read them
+  uint64_t* u_full = q_empty + C::QBUF;      // [NU] unit handed over
   uint64_t* u_empty = u_full + C::NU;        // [NU] every role is done with it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + C::NU);
   int32_t* refs = reinterpret_cast<int32_t*>(tmem_slot + 4);  // [NU][2] exponent references of K and V
@@ -159,6 +184,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
+    prefetch_tmap(&tmQ);
     if (SRC != SEQ_PAGED8) {
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
@@ -172,21 +198,26 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       mbar_init(&p_full[i], 8);
       mbar_init(&p_empty[i], 1);
     }
-    mbar_init(q_full, 8);
+    for (int i = 0; i < C::QBUF; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
     mbar_init(o_empty, 8);
     mbar_init(fin, 1);
     for (int i = 0; i < C::NU; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], 9 + (SRC == SEQ_PAGED8 ? C::LOADERS / 32 : 1));
+      mbar_init(&u_empty[i], 10 + (SRC == SEQ_PAGED8 ? C::LOADERS / 32 : 0));
     }
     fence_mbar_init();
   }
+  // nothing of the kernels before is read above, and no TMEM is taken that they may still need
+  cudaGridDependencySynchronize();
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
-  const SeqPlace place = seq_place<SeqPlan<R, KB, SRC>, C::THREADS>(a, blockIdx.x, pieces, reinterpret_cast<int64_t*>(red), blockIdx.x == 0);
+  const SeqPlace place = seq_place<SeqPlan<0, KB, SRC>, C::THREADS>(a, blockIdx.x, pieces, reinterpret_cast<int64_t*>(red), blockIdx.x == 0);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -207,7 +238,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   if (warp == 2) {
     // -------------------------------------------------------------- walker
     if (lane == 0) {
-      SeqWalk<SeqPlan<R, KB, SRC>> w;
+      SeqWalk<SeqPlan<0, KB, SRC>> w;
       w.start(a, place);
       bool left = false;  // a unit left unfinished
       for (;;) {
@@ -221,19 +252,33 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         if (!more) break;
         if (ws && w.u.j0 == 0 && w.u.j1 < w.u.nb) {
           left = true;
-          seq_leave_note<R, D>(ws, blockIdx.x, w.u, w.u.q_begin, R, group, place.per, false);
+          seq_leave_note<R, D>(ws, blockIdx.x, w.u, w.u.q_begin, a.tile, group, place.per, false);
         }
         w.advance(a);
       }
-      if (ws && !left) seq_leave_note<R, D>(ws, blockIdx.x, w.u, 0, R, 1, place.per, true);
+      if (ws && !left) seq_leave_note<R, D>(ws, blockIdx.x, w.u, 0, a.tile, 1, place.per, true);
     }
-  } else if (warp == 0 && SRC != SEQ_PAGED8) {
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
+      int s = 0, qs = 0;
+      uint32_t ph = 0, qph = 0;
       bool ok = true;
       SeqUnit u;
+      const int tokens = a.tile / group;  // per Q tile: its rows are (token, head) with the head first
+      auto load_q = [&]() -> bool {
+        if (!mbar_wait(&q_empty[qs], qph ^ 1u, status)) return false;
+        mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(a.tile * D * 2));
+#pragma unroll
+        for (int bx = 0; bx < C::NBOX; ++bx)
+          tma_load_3d(&tmQ, &q_full[qs], sQ + qs * C::TILEB + bx * C::BOXB, bx * C::BW, u.h * group,
+                      static_cast<int32_t>(u.q_begin) + u.t * tokens);
+        if (++qs == C::QBUF) {
+          qs = 0;
+          qph ^= 1u;
+        }
+        return true;
+      };
       auto load = [&](const CUtensorMap* tm, int j) -> bool {
         if (!mbar_wait(&kv_empty[s], ph ^ 1u, status)) return false;
         uint8_t* dst = tiles + s * C::TILEB;
@@ -274,18 +319,24 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         return true;
       };
       while (ok && unit_take(u)) {
-        const int j1 = seq_real_end(a, u, group, R, KB);
-        for (int j = u.j0; ok && j < j1; ++j) {
-          if (j == u.j0) ok = load(&tmK, j);
-          if (ok && j + 1 < j1) ok = load(&tmK, j + 1);
-          if (ok) ok = load(&tmV, j);
+        const int j1 = seq_real_end(a, u, group, a.tile, KB);
+        if (u.j0 < j1) ok = load_q();
+        if constexpr (SRC != SEQ_PAGED8) {
+          for (int j = u.j0; ok && j < j1; ++j) {
+            if (j == u.j0) ok = load(&tmK, j);
+            if (ok && j + 1 < j1) ok = load(&tmK, j + 1);
+            if (ok) ok = load(&tmV, j);
+          }
         }
         unit_done();
         ++ui;
       }
       // copies already issued must land before the block exits (a failed wait left some behind)
-      if (status_set(status))
-        for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
+      if (status_set(status)) {
+        for (int i = 0; i < C::QBUF; ++i) mbar_drain(&q_full[i], qph ^ (i < qs ? 0u : 1u), status);
+        if (SRC != SEQ_PAGED8)
+          for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
+      }
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
@@ -294,8 +345,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     const bool bf = Half16<T>::kBF16;
     const uint32_t idS = idesc_f16kind_f32(R, KB, 0, 0, bf);
     const uint32_t idO = idesc_f16kind_f32(R, D, 0, 1, bf);
-    int s = 0;
-    uint32_t ph = 0, g = 0, uc = 0;
+    int s = 0, qs = 0;
+    uint32_t ph = 0, qph = 0, g = 0, uc = 0;
     bool ok = true;
     SeqUnit u;
     auto step = [&]() {
@@ -304,19 +355,21 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         ph ^= 1u;
       }
     };
-    auto issue_s = [&](uint32_t gb) -> bool {
+    auto issue_s = [&](uint32_t gb, bool last) -> bool {
       if (!mbar_wait(&kv_full[s], ph, status)) return false;
       if (elect_one()) {
         tc_fence_after();
-        const uint32_t ka = smem_u32(tiles + s * C::TILEB);
+        const uint32_t ka = smem_u32(tiles + s * C::TILEB), qa = smem_u32(sQ + qs * C::TILEB);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
           const uint64_t bd = smem_desc(ka + bx * C::BOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
-          whale_umma_ts(tmem + (gb & 1u) * KB, tmem + C::QCOL + ks * 8, bd, idS, ks != 0 ? 1u : 0u);
+          const uint64_t ad = smem_desc(qa + bx * C::BOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
+          umma_f16kind(tmem + (gb & 1u) * KB, ad, bd, idS, ks != 0 ? 1u : 0u);
         }
         umma_commit(&s_full[gb & 1u]);
         umma_commit(&kv_empty[s]);
+        if (last) umma_commit(&q_empty[qs]);
       }
       __syncwarp();
       step();
@@ -352,18 +405,22 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       return true;
     };
     while (ok && unit_take(u)) {
-      const int j1 = seq_real_end(a, u, group, R, KB);
+      const int j1 = seq_real_end(a, u, group, a.tile, KB);
       if (u.j0 < j1) {
-        ok = mbar_wait(q_full, uc & 1u, status);
-        if (ok) ok = issue_s(g);
+        ok = mbar_wait(&q_full[qs], qph, status);
+        if (ok) ok = issue_s(g, u.j0 + 1 == j1);
         for (int j = u.j0; ok && j < j1; ++j) {
-          if (j + 1 < j1) ok = issue_s(g + 1u);
+          if (j + 1 < j1) ok = issue_s(g + 1u, j + 2 == j1);
           // O is free once the softmax warps have read the unit before
           if (ok && j == u.j0 && uc > 0) ok = mbar_wait(o_empty, (uc - 1u) & 1u, status);
           if (ok) ok = issue_pv(j, j + 1 == j1, g, j == u.j0);
           ++g;
         }
         ++uc;
+        if (++qs == C::QBUF) {
+          qs = 0;
+          qph ^= 1u;
+        }
       }
       __syncwarp();
       if (lane == 0) unit_done();
@@ -393,39 +450,15 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const bool got = ok && unit_take(u);
       if (!named_bar_and(bar_id, 64, got)) break;
       __syncwarp();
-      const int j1 = seq_real_end(a, u, group, R, KB);
-      const int r = u.t * R + row;  // packed row of the sequence
-      const bool warp_on = u.t * R + q * 32 < u.rows;
-      const bool row_on = r < u.rows;
+      const int j1 = seq_real_end(a, u, group, a.tile, KB);
+      const int r = u.t * a.tile + row;  // packed row of the sequence
+      const bool warp_on = q * 32 < a.tile && u.t * a.tile + q * 32 < u.rows;
+      const bool row_on = row < a.tile && r < u.rows;
       const int qi = row_on ? r / group : 0, qh = u.h * group + (row_on ? r % group : 0);
       const int seen = row_on ? seq_seen(u.len, u.n, qi, a.causal) : INT32_MAX;
       const bool whole = u.j0 == 0 && u.j1 == u.nb;
       const int64_t orow = (u.q_begin + qi) * a.q_heads + qh;
       if (u.j0 < j1) {
-        // the unit's query rows into TMEM (this half's D / 2 columns, as 16-bit pairs)
-        {
-          uint32_t qv[D / 4];
-          if (row_on) {
-            const uint4* src =
-                reinterpret_cast<const uint4*>(Q + (u.q_begin + qi) * a.q_stride + qh * D + half * (D / 2));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint4 v = __ldg(src + i);
-              qv[4 * i] = v.x;
-              qv[4 * i + 1] = v.y;
-              qv[4 * i + 2] = v.z;
-              qv[4 * i + 3] = v.w;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < D / 4; ++i) qv[i] = 0u;
-          }
-          whale_tmem_st_cols<D / 4>(tmem + lane_base + C::QCOL + half * (D / 4), qv);
-          whale_tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(q_full);
-        }
         float m = -INFINITY, l = 0.f;
         float scale_log2 = a.scale * 1.4426950408889634f;
         for (int j = u.j0; j < j1; ++j, ++g) {
@@ -459,18 +492,16 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           for (int pass = 0;; ++pass) {
             if (again) {
               const float nm = mnew == -INFINITY ? 0.f : -mnew;
-              float s4[4] = {0.f, 0.f, 0.f, 0.f};
+              const float2 sc = make_float2(scale_log2, scale_log2), nm2 = make_float2(nm, nm);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
               for (int c2 = 0; c2 < KB / 4; ++c2) {
-                const float x0 = fmaf(__uint_as_float(sr[2 * c2]), scale_log2, nm);
-                const float x1 = fmaf(__uint_as_float(sr[2 * c2 + 1]), scale_log2, nm);
-                const float p0 = whale_ex2(x0);
-                const float p1 = (c2 & 1) ? seq_ex2_poly(x1) : whale_ex2(x1);
-                s4[(2 * c2) & 3] += p0;
-                s4[(2 * c2 + 1) & 3] += p1;
-                pk[c2] = Half16<T>::pack2(p0, p1);
+                const float2 x = seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
+                const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(whale_ex2(x.x), whale_ex2(x.y));
+                sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
+                pk[c2] = Half16<T>::pack2(p.x, p.y);
               }
-              lsum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+              lsum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             if (pass == 1) break;
             const float mh = seq_max<KB / 2>(sr);
@@ -595,7 +626,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const bool got = ok && unit_take(u);
       if (!named_bar_and(5, C::LOADERS, got)) break;
       __syncwarp();
-      const int j1 = seq_real_end(a, u, group, R, KB);
+      const int j1 = seq_real_end(a, u, group, a.tile, KB);
       const int32_t* trow = a.table + static_cast<int64_t>(u.b) * a.table_width;
       int ref[2] = {127, 127};
       if (!Half16<T>::kBF16 && u.j0 < j1) {

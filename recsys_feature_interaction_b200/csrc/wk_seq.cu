@@ -104,13 +104,15 @@ void cache_args(SeqArgs* a, const wk_cache& c, const int32_t* table, int32_t wid
 
 // ---------------------------------------------------------------- launches
 
-// A kernel that may start while the one before it on the stream ends (it waits for its results
-// itself).
+// Launches a kernel that may start while the one before it on the stream ends: every kernel here
+// waits for that one's results itself, before its first access to global memory. Its launch and set-up
+// (barriers, TMEM) then lie under the end of the kernel before.
 template <typename... P, typename... A>
-wk_status launch_dependent(void (*fn)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... args) {
+wk_status launch(void (*fn)(P...), dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -123,6 +125,10 @@ wk_status launch_dependent(void (*fn)(P...), unsigned grid, unsigned threads, cu
   }
   return WK_OK;
 }
+
+// Up to this many blocks of 128 keys (or 64 rows, twice as many) a unit is not cut: joining its parts
+// is one more launch of about 3 us, a block takes a fraction of that.
+constexpr int kUncut = 4;
 
 // ---- the few-rows kernel: packed rows per (sequence, key head) up to 16 (seq_rows.cuh)
 constexpr int kSMs = 148;  // the grids' unit; results do not depend on it
@@ -137,38 +143,40 @@ int64_t slot_bytes(int r, int d, int64_t pieces) {
   return pieces * static_cast<int64_t>(sizeof(SeqNote)) + 2 * pieces * r * (d + 2) * 4;
 }
 
-// Bytes of partial results; none where no sequence has more than one key block.
+bool rows_cut(const SeqArgs& a) { return a.max_kv > kUncut * kRowsKB; }
+// Bytes of partial results.
 int64_t rows_ws(const SeqArgs& a, int d) {
-  if (a.max_kv <= kRowsKB) return 0;
   const int nq = rows_nq(a);
-  return slot_bytes(8 * nq, d, rows_pieces(d, nq));
+  return rows_cut(a) ? slot_bytes(8 * nq, d, rows_pieces(d, nq)) : 0;
 }
 
 template <int D, typename T, int SRC, int NQ>
-wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* lse, float* ws, const SeqArgs& a,
+wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* lse, float* ws, SeqArgs a,
                    cudaStream_t st) {
-  const int64_t pieces = rows_pieces(D, NQ);
-  const bool cut = a.max_kv > kRowsKB;
-  seq_rows_kernel<D, T, SRC, NQ><<<static_cast<unsigned>(pieces), SEQ_ROWS_THREADS, 0, st>>>(
-      static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse, cut ? ws : nullptr, a, pieces);
-  const wk_status s = launch_status();
-  if (s != WK_OK || !cut) return s;
-  return launch_dependent(seq_combine_kernel<8 * NQ, 8 * NQ, D, T>, static_cast<unsigned>(pieces),
-                          SEQ_COMBINE_THREADS, st, ws, static_cast<T*>(O), lse, a.q_heads,
-                          static_cast<int32_t>(pieces));
+  const int32_t pieces = rows_pieces(D, NQ);
+  a.uncut = !rows_cut(a);
+  const wk_status s = launch(seq_rows_kernel<D, T, SRC, NQ>, pieces, SEQ_ROWS_THREADS, 0, st, static_cast<const T*>(Q), K,
+                             V, static_cast<T*>(O), lse, a.uncut ? nullptr : ws, a, pieces);
+  if (s != WK_OK || a.uncut) return s;
+  return launch(seq_combine_kernel<8 * NQ, 8 * NQ, D, T>, pieces, SEQ_COMBINE_THREADS, 0, st, ws, static_cast<T*>(O),
+                lse, a.q_heads, pieces);
 }
 
 // ---- the tile kernel: any number of rows, 128 packed rows per tile (seq_tile.cuh)
-int64_t tile_ws(const SeqArgs& a, int d) { return a.max_kv <= 128 ? 0 : slot_bytes(128, d, kSMs); }
+bool tile_cut(const SeqArgs& a) { return a.max_kv > kUncut * 128; }
+int64_t tile_ws(const SeqArgs& a, int d) { return tile_cut(a) ? slot_bytes(128, d, kSMs) : 0; }
 
-// [tokens, heads, d] as a 3-D map (d, heads, tokens) with boxes (bw, 1, rows).
+// [tokens, heads, d] as a 3-D map (d, heads, tokens) with boxes (bw, box_heads, box_tokens). Of no
+// tokens it is a map over `any`, and not used.
 template <typename T>
-bool map_tokens(const DevInfo* dv, CUtensorMap* m, const void* base, int d, int heads, int64_t tokens, int64_t stride,
-                int bw, int rows) {
-  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
+bool map_tokens(const DevInfo* dv, CUtensorMap* m, const void* base, const void* any, int d, int heads, int64_t tokens,
+                int64_t stride, int bw, int box_heads, int box_tokens) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(std::max<int64_t>(tokens, 1))};
   const uint64_t strides[2] = {static_cast<uint64_t>(d) * 2, static_cast<uint64_t>(stride) * 2};
-  const uint32_t box[3] = {static_cast<uint32_t>(bw), 1u, static_cast<uint32_t>(rows)};
-  return make_map(dv, m, tmap_dtype<T>(), 3, base, dims, strides, box,
+  const uint32_t box[3] = {static_cast<uint32_t>(bw), static_cast<uint32_t>(box_heads),
+                           static_cast<uint32_t>(box_tokens)};
+  return make_map(dv, m, tmap_dtype<T>(), 3, tokens > 0 ? base : any, dims, strides, box,
                   bw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
@@ -184,16 +192,18 @@ bool map_pages(const DevInfo* dv, CUtensorMap* m, const void* base, int d, int64
 
 template <int D, typename T, int SRC>
 wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* V, void* O, float* lse, float* ws,
-                   const SeqArgs& a, cudaStream_t st) {
+                   SeqArgs a, cudaStream_t st) {
   using C = StCfg<D, SRC>;
-  CUtensorMap mk{}, mv{};
-  if (SRC == SEQ_JAGGED && a.total_kv > 0) {
-    if (!map_tokens<T>(dv, &mk, K, D, a.kv_heads, a.total_kv, a.k_stride, C::BW, 128) ||
-        !map_tokens<T>(dv, &mv, V, D, a.kv_heads, a.total_kv, a.v_stride, C::BW, 128))
+  const int group = a.q_heads / a.kv_heads;
+  a.tile = group * (128 / group);
+  a.uncut = !tile_cut(a);
+  CUtensorMap mq{}, mk{}, mv{};
+  if (!map_tokens<T>(dv, &mq, Q, Q, D, a.q_heads, a.total_q, a.q_stride, C::BW, group, 128 / group))
+    return WK_ERR_UNSUPPORTED;
+  if (SRC == SEQ_JAGGED) {
+    if (!map_tokens<T>(dv, &mk, K, Q, D, a.kv_heads, a.total_kv, a.k_stride, C::BW, 1, 128) ||
+        !map_tokens<T>(dv, &mv, V, Q, D, a.kv_heads, a.total_kv, a.v_stride, C::BW, 1, 128))
       return WK_ERR_UNSUPPORTED;
-  } else if (SRC == SEQ_JAGGED) {  // no keys at all: the maps are not used
-    if (!map_tokens<T>(dv, &mk, Q, D, 1, 1, D, C::BW, 128)) return WK_ERR_UNSUPPORTED;
-    mv = mk;
   } else if (SRC == SEQ_PAGED16) {
     const int64_t rows = (static_cast<int64_t>(a.num_pages) * a.kv_heads) << a.page_shift;
     if (rows > INT32_MAX || !map_pages<T>(dv, &mk, K, D, rows, C::BW, 1 << a.page_shift) ||
@@ -203,15 +213,12 @@ wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* 
   auto fn = seq_tile_kernel<D, T, SRC>;
   wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
   if (s != WK_OK) return s;
-  const int64_t pieces = kSMs;
-  const bool cut = a.max_kv > 128;
-  fn<<<kSMs, C::THREADS, C::SMEM, st>>>(mk, mv, static_cast<const T*>(Q), K, V, static_cast<T*>(O), lse,
-                                        cut ? ws : nullptr, a, pieces);
-  s = launch_status();
-  if (s != WK_OK || !cut) return s;
+  s = launch(fn, kSMs, C::THREADS, C::SMEM, st, mq, mk, mv, K, V, static_cast<T*>(O), lse, a.uncut ? nullptr : ws, a,
+             int64_t{kSMs});
+  if (s != WK_OK || a.uncut) return s;
   constexpr int CR = 16;
-  return launch_dependent(seq_combine_kernel<128, CR, D, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, st, ws,
-                          static_cast<T*>(O), lse, a.q_heads, static_cast<int32_t>(pieces));
+  return launch(seq_combine_kernel<128, CR, D, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, 0, st, ws,
+                static_cast<T*>(O), lse, a.q_heads, int32_t{kSMs});
 }
 
 int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : tile_ws(a, d); }
@@ -255,7 +262,12 @@ struct RunForward {
 // ---- the backward (seq_back.cuh): delta [total_q, q_heads], then the partial results, which the
 // two kernels use one after the other
 int64_t delta_bytes(const SeqArgs& a) { return (a.total_q * a.q_heads * 4 + 255) / 256 * 256; }
-int64_t backward_ws(const SeqArgs& a, int d) { return delta_bytes(a) + slot_bytes(128, 2 * d, kSMs); }
+int dkv_block(const SeqArgs& a) { return (a.q_heads / a.kv_heads) * (64 / (a.q_heads / a.kv_heads)); }
+bool dq_cut(const SeqArgs& a) { return a.max_kv > 2 * kUncut * 64; }
+bool dkv_cut(const SeqArgs& a) { return packed_rows(a) > 2 * kUncut * dkv_block(a); }
+int64_t backward_ws(const SeqArgs& a, int d) {
+  return delta_bytes(a) + (dkv_cut(a) ? slot_bytes(128, 2 * d, kSMs) : dq_cut(a) ? slot_bytes(128, d, kSMs) : 0);
+}
 
 struct RunBackward {
   const DevInfo* dv;
@@ -272,19 +284,18 @@ struct RunBackward {
     SeqArgs x = a;
     const int group = a.q_heads / a.kv_heads;
     x.tile = DKV ? 128 : group * (128 / group);
-    x.block = DKV ? group * (64 / group) : 64;
+    x.block = DKV ? dkv_block(a) : 64;
+    x.uncut = !(DKV ? dkv_cut(a) : dq_cut(a));
     auto fn = seq_back_kernel<D, T, DKV>;
     wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
     if (s != WK_OK) return s;
-    const int64_t pieces = kSMs;
-    fn<<<kSMs, C::THREADS, C::SMEM, st>>>(m[0], m[1], m[2], m[3], static_cast<const T*>(O), static_cast<const T*>(dO),
-                                          lse, delta, static_cast<T*>(G1), static_cast<T*>(G2), slots, x, pieces);
-    s = launch_status();
-    if (s != WK_OK) return s;
+    s = launch(fn, kSMs, C::THREADS, C::SMEM, st, m[0], m[1], m[2], m[3], static_cast<const T*>(O),
+               static_cast<const T*>(dO), lse, delta, static_cast<T*>(G1), static_cast<T*>(G2),
+               x.uncut ? nullptr : slots, x, int64_t{kSMs});
+    if (s != WK_OK || x.uncut) return s;
     constexpr int CR = 16;
-    return launch_dependent(seq_sum_kernel<CR, D, C::NACC, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, st, slots,
-                            static_cast<T*>(G1), static_cast<T*>(G2), DKV ? a.kv_heads : a.q_heads,
-                            static_cast<int32_t>(pieces));
+    return launch(seq_sum_kernel<CR, D, C::NACC, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, 0, st, slots,
+                  static_cast<T*>(G1), static_cast<T*>(G2), DKV ? a.kv_heads : a.q_heads, int32_t{kSMs});
   }
 
   template <int D, typename T>
@@ -293,23 +304,17 @@ struct RunBackward {
     const int group = a.q_heads / a.kv_heads;
     // without rows (or without keys) the tensors may be NULL; their maps are then not used
     const void* any = a.total_q > 0 ? Q : K;
-    auto map = [&](CUtensorMap* m, const void* p, int heads, int64_t tokens, int64_t stride, int box_heads, int box_tokens) {
-      const uint64_t dims[3] = {D, static_cast<uint64_t>(heads), static_cast<uint64_t>(std::max<int64_t>(tokens, 1))};
-      const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(stride) * 2};
-      const uint32_t box[3] = {BW, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_tokens)};
-      return make_map(dv, m, tmap_dtype<T>(), 3, tokens > 0 ? p : any, dims, strides, box,
-                      BW == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
-    };
     const int64_t od = static_cast<int64_t>(a.q_heads) * D;
+    auto rows = [&](CUtensorMap* m, const void* p, int64_t stride, int n) {
+      return map_tokens<T>(dv, m, p, any, D, a.q_heads, a.total_q, stride, BW, group, n / group);
+    };
+    auto keys = [&](CUtensorMap* m, const void* p, int64_t stride, int n) {
+      return map_tokens<T>(dv, m, p, any, D, a.kv_heads, a.total_kv, stride, BW, 1, n);
+    };
     CUtensorMap q[4], k[4];  // the maps of DQ and of DKV
-    if (!map(&q[0], Q, a.q_heads, a.total_q, a.q_stride, group, 128 / group) ||
-        !map(&q[1], dO, a.q_heads, a.total_q, od, group, 128 / group) ||
-        !map(&q[2], K, a.kv_heads, a.total_kv, a.k_stride, 1, 64) ||
-        !map(&q[3], V, a.kv_heads, a.total_kv, a.v_stride, 1, 64) ||
-        !map(&k[0], K, a.kv_heads, a.total_kv, a.k_stride, 1, 128) ||
-        !map(&k[1], V, a.kv_heads, a.total_kv, a.v_stride, 1, 128) ||
-        !map(&k[2], Q, a.q_heads, a.total_q, a.q_stride, group, 64 / group) ||
-        !map(&k[3], dO, a.q_heads, a.total_q, od, group, 64 / group))
+    if (!rows(&q[0], Q, a.q_stride, 128) || !rows(&q[1], dO, od, 128) || !keys(&q[2], K, a.k_stride, 64) ||
+        !keys(&q[3], V, a.v_stride, 64) || !keys(&k[0], K, a.k_stride, 128) || !keys(&k[1], V, a.v_stride, 128) ||
+        !rows(&k[2], Q, a.q_stride, 64) || !rows(&k[3], dO, od, 64))
       return WK_ERR_UNSUPPORTED;
     float* delta = static_cast<float*>(workspace);
     float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes(a));
@@ -321,9 +326,8 @@ struct RunBackward {
       const wk_status s = one<D, T, true>(k, delta, slots, dK, dV);
       if (s != WK_OK) return s;
       if (a.kv_lens) {
-        seq_zero_padding_kernel<T><<<dim3(static_cast<unsigned>(a.batch), 2), 256, 0, st>>>(
-            static_cast<T*>(dK), static_cast<T*>(dV), static_cast<int64_t>(a.kv_heads) * D, a);
-        return launch_status();
+        return launch(seq_zero_padding_kernel<T>, dim3(static_cast<unsigned>(a.batch), 2), 256, 0, st,
+                      static_cast<T*>(dK), static_cast<T*>(dV), static_cast<int64_t>(a.kv_heads) * D, a);
       }
     }
     return WK_OK;
@@ -341,11 +345,10 @@ struct RunWrite {
   wk_status operator()() const {
     const T *k = static_cast<const T*>(K), *v = static_cast<const T*>(V);
     if (c.dtype == WK_E4M3)
-      cache_write_kernel<D, T, true><<<grid, SEQ_COPY_THREADS, 0, st>>>(k, v, c.K, c.V, c.K_exp, c.V_exp, a, chunks);
-    else
-      cache_write_kernel<D, T, false>
-          <<<grid, SEQ_COPY_THREADS, 0, st>>>(k, v, c.K, c.V, nullptr, nullptr, a, chunks);
-    return launch_status();
+      return launch(cache_write_kernel<D, T, true>, grid, SEQ_COPY_THREADS, 0, st, k, v, c.K, c.V, c.K_exp, c.V_exp, a,
+                    chunks);
+    return launch(cache_write_kernel<D, T, false>, grid, SEQ_COPY_THREADS, 0, st, k, v, c.K, c.V, nullptr, nullptr, a,
+                  chunks);
   }
 };
 
@@ -360,10 +363,8 @@ struct RunRead {
   wk_status operator()() const {
     T *k = static_cast<T*>(K), *v = static_cast<T*>(V);
     if (c.dtype == WK_E4M3)
-      cache_read_kernel<D, T, SEQ_PAGED8><<<grid, SEQ_COPY_THREADS, 0, st>>>(c.K, c.V, k, v, a, chunks);
-    else
-      cache_read_kernel<D, T, SEQ_PAGED16><<<grid, SEQ_COPY_THREADS, 0, st>>>(c.K, c.V, k, v, a, chunks);
-    return launch_status();
+      return launch(cache_read_kernel<D, T, SEQ_PAGED8>, grid, SEQ_COPY_THREADS, 0, st, c.K, c.V, k, v, a, chunks);
+    return launch(cache_read_kernel<D, T, SEQ_PAGED16>, grid, SEQ_COPY_THREADS, 0, st, c.K, c.V, k, v, a, chunks);
   }
 };
 
