@@ -39,6 +39,7 @@ struct SbCfg {
   static constexpr int BW = (D % 64 == 0) ? 64 : 32;
   static constexpr int SWB = BW * 2;
   static constexpr uint32_t SWMODE = BW == 64 ? 2u : 4u;
+  static constexpr uint32_t DESC_HI = seq_desc_hi(8 * SWB, SWMODE);
   static constexpr int NBOX = D / BW;
   static constexpr int ABOXB = R * SWB, YBOXB = YB * SWB;
   static constexpr int AB = NBOX * ABOXB, YBYTES = NBOX * YBOXB;  // one tile that stands / goes by
@@ -252,16 +253,16 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       }
       if (elect_one()) {
         tc_fence_after();
-        const uint32_t aa = smem_u32(sA + 2 * sb * C::AB), ya = smem_u32(sY + 2 * ts * C::YBYTES);
+        const uint32_t x = seq_desc_lo(smem_u32(sA + 2 * sb * C::AB), 16);
+        const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * ts * C::YBYTES), 16);
         const uint32_t t1 = tmem + (gb % C::TB) * 128;
 #pragma unroll
         for (int w = 0; w < 2; ++w)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
-            const uint64_t ad = smem_desc(aa + w * C::AB + bx * C::ABOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
-            const uint64_t bd = smem_desc(ya + w * C::YBYTES + bx * C::YBOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
-            umma_f16kind(t1 + w * 64, ad, bd, idT, ks != 0 ? 1u : 0u);
+            seq_mma_ss<C::DESC_HI>(t1 + w * 64, x + ((w * C::AB + bx * C::ABOXB + kin * 32) >> 4),
+                                   y + ((w * C::YBYTES + bx * C::YBOXB + kin * 32) >> 4), idT, ks != 0 ? 1u : 0u);
           }
         umma_commit(&t_full[gb % C::TB]);
       }
@@ -276,18 +277,15 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       if (!mbar_wait(&p_full[gb % C::TB], (gb / C::TB) & 1u, status)) return false;
       if (elect_one()) {
         tc_fence_after();
-        const uint32_t ya = smem_u32(sY + 2 * as * C::YBYTES);
+        const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * as * C::YBYTES), C::YBOXB);  // MN-major
         const uint32_t t1 = tmem + (gb % C::TB) * 128;
         // columns 16 ks .. + 15 of P (dS): 8 TMEM columns, those of the second 32 behind T's 32nd
 #pragma unroll
         for (int ks = 0; ks < C::YB / 16; ++ks) {
-          const uint32_t at = (ks / 2) * 32 + (ks % 2) * 8;
-          if constexpr (DKV) {
-            const uint64_t d2 = smem_desc(ya + C::YBYTES + ks * 16 * C::SWB, C::YBOXB, 8 * C::SWB, C::SWMODE);
-            whale_umma_ts(tmem + C::ACOL + D, t1 + at, d2, idA, (!first || ks) ? 1u : 0u);  // dV += P^T dO
-          }
-          const uint64_t d1 = smem_desc(ya + ks * 16 * C::SWB, C::YBOXB, 8 * C::SWB, C::SWMODE);
-          whale_umma_ts(tmem + C::ACOL, t1 + 64 + at, d1, idA, (!first || ks) ? 1u : 0u);  // dQ += dS K, dK += dS^T Q
+          const uint32_t at = (ks / 2) * 32 + (ks % 2) * 8, yk = y + ((ks * 16 * C::SWB) >> 4);
+          if constexpr (DKV)  // dV += P^T dO
+            seq_mma_ts<C::DESC_HI>(tmem + C::ACOL + D, t1 + at, yk + (C::YBYTES >> 4), idA, (!first || ks) ? 1u : 0u);
+          seq_mma_ts<C::DESC_HI>(tmem + C::ACOL, t1 + 64 + at, yk, idA, (!first || ks) ? 1u : 0u);  // dQ, dK
         }
         umma_commit(&y_empty[as]);
       }

@@ -3,8 +3,8 @@
 //
 // A block holds up to 128 packed query rows (whole tokens of the query heads that share a key head)
 // and walks 128-key blocks: S = Q K^T from shared memory, softmax weights from TMEM by two warps per lane quarter,
-// P written over S's columns, O += P V with the V tile MN-major. S is double-buffered, S of the
-// next block is issued before P V of this one, K and V tiles arrive in one ring in the order in
+// P written over S's columns, O += P V with the V tile MN-major. S has two or three
+// buffers and runs one or two blocks ahead of P V; K and V tiles arrive in one ring in the order in
 // which the products use them (K0, K1, V0, K2, V1, ..).
 //
 // Roles: warp 0 lane 0 loads tiles with TMA (jagged: 128 rows from the sequence's first; a 16-bit
@@ -41,6 +41,22 @@ __device__ __forceinline__ bool named_bar_and(int id, int count, bool p) {
   return r != 0u;
 }
 
+// Arrives at a barrier over `count` threads without waiting.
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// 32 TMEM lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // True for one thread of a converged warp, always the same one. The MMAs of a warp that runs as a
 // whole are issued under it: with a plain lane == 0 the compiler does not know that one thread is
 // left, and the tensor pipe falls behind when the softmax warps keep the issue slots busy (18 MMAs
@@ -49,6 +65,37 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0u;
+}
+
+// Shared-memory descriptors (see smem_desc) in two words: the upper one is a constant of the layout,
+// the lower one moves with the address by additions. With the whole descriptor rebuilt for each MMA
+// the issuing thread, which shares its scheduler with the softmax warps, falls behind the tensor pipe
+// (18 MMAs of a block next to a softmax loop: 1680 cycles, so 1424).
+constexpr uint32_t seq_desc_hi(uint32_t sbo_bytes, uint32_t swizzle_mode) {
+  return (sbo_bytes >> 4) | (1u << 14) | (swizzle_mode << 29);
+}
+__device__ __forceinline__ uint32_t seq_desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | ((lbo_bytes >> 4) << 16);
+}
+
+// D[tmem] (+)= A B^T, kind::f16, operands in shared memory, or A in TMEM.
+template <uint32_t HI>
+__device__ __forceinline__ void seq_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(add), "n"(HI)
+      : "memory");
+}
+template <uint32_t HI>
+__device__ __forceinline__ void seq_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(add), "n"(HI)
+      : "memory");
 }
 
 // max(a, b, c) and max(a, b) that give NaN if an operand is NaN.
@@ -119,6 +166,7 @@ struct StCfg {
   static constexpr int BW = (D % 64 == 0) ? 64 : 32;     // columns per box
   static constexpr int SWB = BW * 2;                     // bytes per box row = swizzle span
   static constexpr uint32_t SWMODE = BW == 64 ? 2u : 4u;
+  static constexpr uint32_t DESC_HI = seq_desc_hi(8 * SWB, SWMODE);
   static constexpr int NBOX = D / BW;
   static constexpr int BOXB = KB * SWB;
   static constexpr int TILEB = NBOX * BOXB;              // one K or V tile
@@ -126,7 +174,7 @@ struct StCfg {
   static constexpr int NU = 4;                           // units in flight between the walker and the roles
   static constexpr int BARB = 512;                       // barriers, TMEM address, references
   static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
-  static constexpr int REDB = 4 * R * 4;                 // softmax pair exchange [2 parities][2 halves][R]
+  static constexpr int REDB = 4 * R * 4;                 // what the softmax groups tell each other, per row
   static constexpr int FIXED = BARB + UNITB + REDB;
   static constexpr int QBUF = D <= 128 ? 2 : 1;          // Q tiles in flight: d = 160 has no room for two
   static constexpr int STAGES_RAW = (LIMIT - FIXED - QBUF * TILEB) / TILEB;
@@ -134,12 +182,15 @@ struct StCfg {
   // more than half an SM's shared memory: one block per SM, whose 512 TMEM columns are its own
   static constexpr int RAW = FIXED + (QBUF + STAGES) * TILEB;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
-  // TMEM: S0, S1 [0, 256) (P over their first 64 columns), O [256, 256 + D)
-  static constexpr int OCOL = 2 * KB;
+  // TMEM: NS buffers of S (P over their first 64 columns), then O. With three, S runs two blocks
+  // ahead of P V, and a softmax group finds its next block ready; d = 160 has room for two.
+  static constexpr int NS = D <= 128 ? 3 : 2;
+  static constexpr int AHEAD = NS - 1;
+  static constexpr int OCOL = NS * KB;
   static constexpr int THREADS = SRC == SEQ_PAGED8 ? 512 : 384;
   static constexpr int LOADERS = 128;
   static_assert(OCOL + D <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
-  static_assert((2 * STAGES + 8 + 2 * QBUF + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
+  static_assert((2 * STAGES + 4 * NS + 2 + 2 * QBUF + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
 };
 
 // Key blocks [j0, j1) of a unit that hold keys (a unit without keys has a cost, but no block).
@@ -165,12 +216,12 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::TILEB);
   uint64_t* kv_full = bars;                  // [STAGES] tile landed
   uint64_t* kv_empty = bars + C::STAGES;     // [STAGES] its product has read it
-  uint64_t* s_full = bars + 2 * C::STAGES;   // [2] S in TMEM
-  uint64_t* p_full = s_full + 2;             // [2] P in TMEM
-  uint64_t* p_empty = s_full + 4;            // [2] P V has read it (so O holds that block)
-  uint64_t* o_empty = s_full + 6;            // O read by the softmax warps (per unit)
-  uint64_t* fin = s_full + 7;
-  uint64_t* q_full = s_full + 8;             // [QBUF] the unit's Q rows landed
+  uint64_t* s_full = bars + 2 * C::STAGES;   // [NS] S in TMEM
+  uint64_t* p_full = s_full + C::NS;         // [NS][2] the halves of P in TMEM
+  uint64_t* p_empty = p_full + 2 * C::NS;    // [NS] P V has read it (so O holds that block)
+  uint64_t* o_empty = p_empty + C::NS;       // O read by the softmax warps (per unit)
+  uint64_t* fin = o_empty + 1;
+  uint64_t* q_full = fin + 1;                // [QBUF] the unit's Q rows landed
   uint64_t* q_empty = q_full + C::QBUF;      // [QBUF] its last S has read them
   uint64_t* u_full = q_empty + C::QBUF;      // [NU] unit handed over
   uint64_t* u_empty = u_full + C::NU;        // [NU] every role is done with it
@@ -193,9 +244,10 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       mbar_init(&kv_full[s], SRC == SEQ_PAGED8 ? C::LOADERS / 32 : 1);
       mbar_init(&kv_empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NS; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&p_empty[i], 1);
     }
     for (int i = 0; i < C::QBUF; ++i) {
@@ -260,88 +312,101 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int s = 0, qs = 0;
-      uint32_t ph = 0, qph = 0;
-      bool ok = true;
-      SeqUnit u;
-      const int tokens = a.tile / group;  // per Q tile: its rows are (token, head) with the head first
-      auto load_q = [&]() -> bool {
-        if (!mbar_wait(&q_empty[qs], qph ^ 1u, status)) return false;
+    // The whole warp walks, one thread issues. With a cache each lane holds one page of a window of
+    // 32, one for K and one for V (K runs ahead), so that a tile does not wait for its table entries.
+    int s = 0, qs = 0;
+    uint32_t ph = 0, qph = 0;
+    bool ok = true;
+    SeqUnit u;
+    const int tokens = a.tile / group;  // per Q tile: its rows are (token, head) with the head first
+    auto load_q = [&]() -> bool {
+      if (!mbar_wait(&q_empty[qs], qph ^ 1u, status)) return false;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(a.tile * D * 2));
 #pragma unroll
         for (int bx = 0; bx < C::NBOX; ++bx)
           tma_load_3d(&tmQ, &q_full[qs], sQ + qs * C::TILEB + bx * C::BOXB, bx * C::BW, u.h * group,
                       static_cast<int32_t>(u.q_begin) + u.t * tokens);
-        if (++qs == C::QBUF) {
-          qs = 0;
-          qph ^= 1u;
+      }
+      __syncwarp();
+      if (++qs == C::QBUF) {
+        qs = 0;
+        qph ^= 1u;
+      }
+      return true;
+    };
+    int win[2] = {-1, -1};    // the windows' numbers (page index / 32) and this lane's page of each
+    int32_t held[2] = {-1, -1};
+    auto load = [&](const CUtensorMap* tm, int which, int j) -> bool {
+      const int ps = 1 << a.page_shift, per = KB >> a.page_shift;  // keys of a page, pages of a tile
+      int np = 0, first = 0;
+      if constexpr (SRC == SEQ_PAGED16) {
+        np = (min(KB, u.len - j * KB) + ps - 1) >> a.page_shift;
+        first = j * per;  // a tile's pages lie in one window
+        if (win[which] != first >> 5) {
+          win[which] = first >> 5;
+          const int64_t pos = (static_cast<int64_t>(win[which]) * 32 + lane) << a.page_shift;
+          held[which] = -1;
+          if (pos < u.len) {
+            held[which] = seq_page(a.table + static_cast<int64_t>(u.b) * a.table_width, pos, a.page_shift, a.num_pages);
+            if (held[which] < 0) flag_error(status, kFlagBadShape);
+          }
         }
-        return true;
-      };
-      auto load = [&](const CUtensorMap* tm, int j) -> bool {
-        if (!mbar_wait(&kv_empty[s], ph ^ 1u, status)) return false;
-        uint8_t* dst = tiles + s * C::TILEB;
-        if constexpr (SRC == SEQ_JAGGED) {
+      }
+      if (!mbar_wait(&kv_empty[s], ph ^ 1u, status)) return false;
+      uint8_t* dst = tiles + s * C::TILEB;
+      if constexpr (SRC == SEQ_JAGGED) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(&kv_full[s], static_cast<uint32_t>(C::TILEB));
 #pragma unroll
           for (int bx = 0; bx < C::NBOX; ++bx)
             tma_load_3d(tm, &kv_full[s], dst + bx * C::BOXB, bx * C::BW, u.h, static_cast<int32_t>(u.kv_begin) + j * KB);
-        } else {
-          const int ps = 1 << a.page_shift;
-          const int32_t* row = a.table + static_cast<int64_t>(u.b) * a.table_width;
-          const int valid = min(KB, u.len - j * KB), np = (valid + ps - 1) >> a.page_shift;
-          int32_t page[8];
-          int good = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            page[i] = -1;
-            if (i < np) {
-              page[i] = seq_page(row, static_cast<int64_t>(j) * KB + i * ps, a.page_shift, a.num_pages);
-              if (page[i] < 0) flag_error(status, kFlagBadShape);
-              else ++good;
-            }
-          }
-          mbar_arrive_expect_tx(&kv_full[s], static_cast<uint32_t>(good * ps * D * 2));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (page[i] < 0) continue;
-            const int32_t r = static_cast<int32_t>(((static_cast<int64_t>(page[i]) * a.kv_heads + u.h) << a.page_shift));
-#pragma unroll
-            for (int bx = 0; bx < C::NBOX; ++bx)
-              tma_load_2d(tm, &kv_full[s], dst + bx * C::BOXB + i * ps * C::SWB, bx * C::BW, r);
-          }
         }
-        if (++s == C::STAGES) {
-          s = 0;
-          ph ^= 1u;
+      } else {
+        const bool mine = lane >= (first & 31) && lane < (first & 31) + np;
+        const int good = __popc(__ballot_sync(0xffffffffu, mine && held[which] >= 0));
+        if (elect_one()) mbar_arrive_expect_tx(&kv_full[s], static_cast<uint32_t>(good * ps * D * 2));
+        __syncwarp();
+        if (mine && held[which] >= 0) {  // the lane that holds a page loads it
+          const int32_t r =
+              static_cast<int32_t>((static_cast<int64_t>(held[which]) * a.kv_heads + u.h) << a.page_shift);
+#pragma unroll
+          for (int bx = 0; bx < C::NBOX; ++bx)
+            tma_load_2d(tm, &kv_full[s], dst + bx * C::BOXB + (lane - (first & 31)) * ps * C::SWB, bx * C::BW, r);
         }
-        return true;
-      };
-      while (ok && unit_take(u)) {
-        const int j1 = seq_real_end(a, u, group, a.tile, KB);
-        if (u.j0 < j1) ok = load_q();
-        if constexpr (SRC != SEQ_PAGED8) {
-          for (int j = u.j0; ok && j < j1; ++j) {
-            if (j == u.j0) ok = load(&tmK, j);
-            if (ok && j + 1 < j1) ok = load(&tmK, j + 1);
-            if (ok) ok = load(&tmV, j);
-          }
-        }
-        unit_done();
-        ++ui;
       }
-      // copies already issued must land before the block exits (a failed wait left some behind)
-      if (status_set(status)) {
-        for (int i = 0; i < C::QBUF; ++i) mbar_drain(&q_full[i], qph ^ (i < qs ? 0u : 1u), status);
-        if (SRC != SEQ_PAGED8)
-          for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
+      __syncwarp();
+      if (++s == C::STAGES) {
+        s = 0;
+        ph ^= 1u;
       }
+      return true;
+    };
+    while (ok && unit_take(u)) {
+      const int j1 = seq_real_end(a, u, group, a.tile, KB);
+      if (u.j0 < j1) ok = load_q();
+      if constexpr (SRC != SEQ_PAGED8) {
+        win[0] = win[1] = -1;
+        for (int j = u.j0; ok && j < j1; ++j) {
+          for (int k = u.j0; ok && j == u.j0 && k < min(j1, u.j0 + C::AHEAD); ++k) ok = load(&tmK, 0, k);
+          if (ok && j + C::AHEAD < j1) ok = load(&tmK, 0, j + C::AHEAD);
+          if (ok) ok = load(&tmV, 1, j);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) unit_done();
+      ++ui;
+    }
+    // copies already issued must land before the block exits (a failed wait left some behind)
+    if (lane == 0 && status_set(status)) {
+      for (int i = 0; i < C::QBUF; ++i) mbar_drain(&q_full[i], qph ^ (i < qs ? 0u : 1u), status);
+      if (SRC != SEQ_PAGED8)
+        for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     // The whole warp walks; one thread issues. The MMAs of a thread run in issue order, so S of block
-    // j + 2 is written into S_j's columns only after P V_j, issued before it, has read P_j there.
+    // j + NS is written into S_j's columns only after P V_j, issued before it, has read P_j there.
     const bool bf = Half16<T>::kBF16;
     const uint32_t idS = idesc_f16kind_f32(R, KB, 0, 0, bf);
     const uint32_t idO = idesc_f16kind_f32(R, D, 0, 1, bf);
@@ -359,15 +424,14 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       if (!mbar_wait(&kv_full[s], ph, status)) return false;
       if (elect_one()) {
         tc_fence_after();
-        const uint32_t ka = smem_u32(tiles + s * C::TILEB), qa = smem_u32(sQ + qs * C::TILEB);
+        const uint32_t k = seq_desc_lo(smem_u32(tiles + s * C::TILEB), 16);
+        const uint32_t qd = seq_desc_lo(smem_u32(sQ + qs * C::TILEB), 16);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
-          const uint64_t bd = smem_desc(ka + bx * C::BOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
-          const uint64_t ad = smem_desc(qa + bx * C::BOXB + kin * 32, 16, 8 * C::SWB, C::SWMODE);
-          umma_f16kind(tmem + (gb & 1u) * KB, ad, bd, idS, ks != 0 ? 1u : 0u);
+          const uint32_t at = ((ks / (C::BW / 16)) * C::BOXB + (ks % (C::BW / 16)) * 32) >> 4;
+          seq_mma_ss<C::DESC_HI>(tmem + (gb % C::NS) * KB, qd + at, k + at, idS, ks != 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[gb & 1u]);
+        umma_commit(&s_full[gb % C::NS]);
         umma_commit(&kv_empty[s]);
         if (last) umma_commit(&q_empty[qs]);
       }
@@ -377,7 +441,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     };
     auto issue_pv = [&](int j, bool last, uint32_t gj, bool first) -> bool {
       if (!mbar_wait(&kv_full[s], ph, status)) return false;
-      const uint32_t va = smem_u32(tiles + s * C::TILEB);
+      // MN-major V: BW-column atoms BOXB apart, 8-key groups 8 * SWB apart
+      const uint32_t v = seq_desc_lo(smem_u32(tiles + s * C::TILEB), C::BOXB);
       const int valid = u.len - j * KB;
       if (SRC != SEQ_PAGED8 && last && valid < KB) {  // rows behind the sequence: their weights are 0
         for (int i = lane; i < (KB - valid) * C::NBOX * (C::SWB / 16); i += 32) {
@@ -388,16 +453,22 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!mbar_wait(&p_full[gj & 1u], (gj >> 1) & 1u, status)) return false;
-      if (elect_one()) {
-        tc_fence_after();
+      const uint32_t buf = gj % C::NS;
 #pragma unroll
-        for (int ks = 0; ks < KB / 16; ++ks) {
-          // MN-major V: BW-column atoms BOXB apart, 8-key groups 8 * SWB apart
-          const uint64_t bd = smem_desc(va + ks * 16 * C::SWB, C::BOXB, 8 * C::SWB, C::SWMODE);
-          whale_umma_ts(tmem + C::OCOL, tmem + (gj & 1u) * KB + ks * 8, bd, idO, (!first || ks) ? 1u : 0u);
+      for (int half = 0; half < 2; ++half) {  // the first half's product runs under the second's softmax
+        if (!mbar_wait(&p_full[2 * buf + half], (gj / C::NS) & 1u, status)) return false;
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int ks = half * KB / 32; ks < (half + 1) * KB / 32; ++ks) {
+            seq_mma_ts<C::DESC_HI>(tmem + C::OCOL, tmem + buf * KB + ks * 8, v + ((ks * 16 * C::SWB) >> 4), idO,
+                                   (!first || ks) ? 1u : 0u);
+          }
         }
-        umma_commit(&p_empty[gj & 1u]);
+        __syncwarp();
+      }
+      if (elect_one()) {
+        umma_commit(&p_empty[buf]);
         umma_commit(&kv_empty[s]);
       }
       __syncwarp();
@@ -408,9 +479,9 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const int j1 = seq_real_end(a, u, group, a.tile, KB);
       if (u.j0 < j1) {
         ok = mbar_wait(&q_full[qs], qph, status);
-        if (ok) ok = issue_s(g, u.j0 + 1 == j1);
+        for (int k = 0; ok && k < min(C::AHEAD, j1 - u.j0); ++k) ok = issue_s(g + k, u.j0 + k + 1 == j1);
         for (int j = u.j0; ok && j < j1; ++j) {
-          if (j + 1 < j1) ok = issue_s(g + 1u, j + 2 == j1);
+          if (j + C::AHEAD < j1) ok = issue_s(g + C::AHEAD, j + C::AHEAD + 1 == j1);
           // O is free once the softmax warps have read the unit before
           if (ok && j == u.j0 && uc > 0) ok = mbar_wait(o_empty, (uc - 1u) & 1u, status);
           if (ok) ok = issue_pv(j, j + 1 == j1, g, j == u.j0);
@@ -433,22 +504,27 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------- softmax
-    // Two warps per TMEM lane quarter: rows 32 q .. + 31, key columns 64 half .. + 63 of each
-    // block. The pair exchanges per-row partial maxima (by block parity) and, at the end of a
-    // unit, partial row sums, through shared memory under 64-thread barriers.
+    // Two groups of four warps take the blocks in turn; a thread has one row and all 128 keys of a
+    // block. So the groups are half a block apart, and one's exponentials
+    // run while the other waits for TMEM. What they share per row is the running maximum: a group
+    // hands its decision on before it computes its weights (an arrive that does not wait), so the
+    // other one finds it there.
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int grp = (warp - 4) >> 2;
     const int row = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    const int bar_id = 1 + q;
+    const int pair_id = 1 + q, hear_id = 6 + q + 4 * (grp ^ 1), tell_id = 6 + q + 4 * grp;
+    float* mrow = red;           // [2][R] running maximum after a group's last block
+    float* lrow = red + 2 * R;   // [2][R] row sums at the end of a unit, relative to mrow
     uint32_t g = 0;
     // After a failed wait a thread stops waiting but walks the unit to its end, so that the
-    // warp-collective TMEM accesses and the pair barriers stay converged; the pair leaves together.
+    // warp-collective TMEM accesses and the barriers stay converged; the pair of warps of a lane
+    // quarter leaves together.
     bool ok = true;
     SeqUnit u;
     for (;;) {
       const bool got = ok && unit_take(u);
-      if (!named_bar_and(bar_id, 64, got)) break;
+      if (!named_bar_and(pair_id, 64, got)) break;
       __syncwarp();
       const int j1 = seq_real_end(a, u, group, a.tile, KB);
       const int r = u.t * a.tile + row;  // packed row of the sequence
@@ -459,105 +535,108 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const bool whole = u.j0 == 0 && u.j1 == u.nb;
       const int64_t orow = (u.q_begin + qi) * a.q_heads + qh;
       if (u.j0 < j1) {
-        float m = -INFINITY, l = 0.f;
-        float scale_log2 = a.scale * 1.4426950408889634f;
+        float m = -INFINITY, l = 0.f;  // this group's row sum, relative to m
         for (int j = u.j0; j < j1; ++j, ++g) {
-          const uint32_t buf = g & 1u;
-          if (ok) ok = mbar_wait(&s_full[buf], (g >> 1) & 1u, status);
+          if ((g & 1u) != static_cast<uint32_t>(grp)) continue;
+          const uint32_t buf = g % C::NS;
+          if (ok) ok = mbar_wait(&s_full[buf], (g / C::NS) & 1u, status);
           tc_fence_after();
-          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16 && j == u.j0)  // known once the first K tile is
-            scale_log2 = a.scale * 1.4426950408889634f * seq_ex2(static_cast<float>(refs[2 * (ui % C::NU)] - 127));
+          float scale_log2 = a.scale * 1.4426950408889634f;
+          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
+            scale_log2 *= seq_ex2(static_cast<float>(refs[2 * (ui % C::NU)] - 127));
+          // Half of the block's scores at a time: the second half's maximum, the first half's, then the
+          // first half's weights, and the second half again (a whole row would not fit the registers).
           uint32_t sr[KB / 2];
-          if (warp_on) {
-            const uint32_t ta = tmem + lane_base + buf * KB + half * (KB / 2);
-            tmem_ld32(ta, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-            tmem_ld32(ta + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-            tmem_ld_wait();
-          }
-          const int kvalid = seen - j * KB - half * (KB / 2);  // this row's keys in this half
-          if (!__all_sync(0xffffffffu, kvalid >= KB / 2)) {
-#pragma unroll
-            for (int c = 0; c < KB / 2; ++c)
-              if (c >= kvalid) sr[c] = 0xFF800000u;  // -inf
-          }
-          // P = 2^(S scale_log2 - m), rounded to the operand type and packed; row sum in fp32. From
-          // the second block of a row on it is computed with the running maximum at once, next to
-          // this block's maximum, and again only if that raises it.
-          const bool spec = j > u.j0;
-          uint32_t pk[KB / 4];
-          float lsum = 0.f, mb = -INFINITY, mnew = m, factor = 1.f;
-          bool redo = false;
-          bool again = warp_on && spec;
-#pragma unroll 1
-          for (int pass = 0;; ++pass) {
-            if (again) {
-              const float nm = mnew == -INFINITY ? 0.f : -mnew;
-              const float2 sc = make_float2(scale_log2, scale_log2), nm2 = make_float2(nm, nm);
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-              for (int c2 = 0; c2 < KB / 4; ++c2) {
-                const float2 x = seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
-                const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(whale_ex2(x.x), whale_ex2(x.y));
-                sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
-                pk[c2] = Half16<T>::pack2(p.x, p.y);
-              }
-              lsum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            }
-            if (pass == 1) break;
-            const float mh = seq_max<KB / 2>(sr);
-            red[(buf * 2 + half) * R + row] = mh;
-            // after this barrier both warps of the pair have read S_j: P_j may overwrite it
-            tc_fence_before();
-            named_bar(bar_id, 64);
-            tc_fence_after();
-            mb = seq_max2(mh, red[(buf * 2 + (half ^ 1)) * R + row]);
-            const float mb2 = mb * scale_log2;
-            const bool need = warp_on && row_on && (mb2 > m + 8.f);
-            if (need) {
-              mnew = mb2;
-              factor = whale_ex2(m - mnew);
-            }
-            redo = warp_on && (!spec || __any_sync(0xffffffffu, need));
-            if (!redo) break;
-            again = true;
-          }
-          if (mnew == -INFINITY) lsum = 0.f;  // no key seen yet
-          if (mb != mb) lsum = mb;  // a NaN score: the polynomial would lose it
-          // P V two blocks back has completed (keeps this waiter within one phase of p_empty)
-          if (ok) ok = mbar_wait(&p_empty[buf], ((g >> 1) & 1u) ^ 1u, status);
-          if (spec && redo) {
-            // the running maximum was raised: O must hold every earlier block before it is rescaled
-            const uint32_t gp = g - 1u;
-            if (ok) ok = mbar_wait(&p_empty[gp & 1u], (gp >> 1) & 1u, status);
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = half; cc < D / 32; cc += 2) {
-              uint32_t o[32];
-              tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
+          const uint32_t ta = tmem + lane_base + buf * KB;
+          const int kvalid = seen - j * KB;  // this row's keys in the block
+          const bool full = __all_sync(0xffffffffu, kvalid >= KB);
+          auto load_half = [&](int at) {
+            if (warp_on) {
+              tmem_ld32(ta + at, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+              tmem_ld32(ta + at + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
               tmem_ld_wait();
+            }
+            if (!full) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-              whale_tmem_st32(tmem + lane_base + C::OCOL + cc * 32, o);
+              for (int c = 0; c < KB / 2; ++c)
+                if (at + c >= kvalid) sr[c] = 0xFF800000u;  // -inf
+            }
+          };
+          load_half(KB / 2);
+          float mh = seq_max<KB / 2>(sr);
+          load_half(0);
+          mh = seq_max2(mh, seq_max<KB / 2>(sr));
+          float mprev = -INFINITY;
+          if (j > u.j0) {
+            named_bar(hear_id, 64);
+            mprev = mrow[(grp ^ 1) * R + row];
+          }
+          const float mb2 = mh * scale_log2;
+          const bool need = row_on && mb2 > mprev + 8.f;
+          const float mnew = need ? mb2 : mprev;
+          if (j + 1 < j1) {
+            mrow[grp * R + row] = mnew;
+            named_bar_arrive(tell_id, 64);
+          }
+          if (j > u.j0 && __any_sync(0xffffffffu, need)) {
+            // the maximum was raised: O must hold every earlier block before it is rescaled
+            const uint32_t gp = g - 1u;
+            if (ok) ok = mbar_wait(&p_empty[gp % C::NS], (gp / C::NS) & 1u, status);
+            tc_fence_after();
+            const float factor = need ? whale_ex2(mprev - mnew) : 1.f;
+            if (warp_on) {
+#pragma unroll 1
+              for (int cc = 0; cc < D / 16; ++cc) {
+                uint32_t o[16];
+                tmem_ld16(tmem + lane_base + C::OCOL + cc * 16, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+                whale_tmem_st_cols<16>(tmem + lane_base + C::OCOL + cc * 16, o);
+              }
             }
           }
-          l = l * factor + lsum;
+          // P = 2^(S scale_log2 - m), rounded to the operand type over S's first 64 columns; row sum
+          // in fp32
+          const float nm = mnew == -INFINITY ? 0.f : -mnew;
+          const float2 sc = make_float2(scale_log2, scale_log2), nm2 = make_float2(nm, nm);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int at = 0; at < KB; at += KB / 2) {
+            if (at) load_half(at);
+            uint32_t pk[KB / 4];
+#pragma unroll
+            for (int c2 = 0; c2 < KB / 4; ++c2) {
+              const float2 x =
+                  seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
+              const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(whale_ex2(x.x), whale_ex2(x.y));
+              sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
+              pk[c2] = Half16<T>::pack2(p.x, p.y);
+            }
+            if (warp_on) whale_tmem_st32(ta + at / 2, pk);
+            whale_tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[2 * buf + (at ? 1 : 0)]);
+          }
+          float lsum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if (mnew == -INFINITY) lsum = 0.f;  // no key seen yet
+          if (mh != mh) lsum = mh;            // a NaN score: the polynomial would lose it
+          l = (m == -INFINITY ? l * 0.f : l * whale_ex2(m - mnew)) + lsum;
           m = mnew;
-          // P_j over the first 64 columns of S_j: keys 64 half .. + 63 in columns 32 half .. + 31
-          if (warp_on) whale_tmem_st32(tmem + lane_base + buf * KB + half * 32, pk);
-          whale_tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[buf]);
         }
-        // the row sums of both halves, through the exchange slot of the parity that the last block
-        // did not use; the second barrier keeps the next unit from overwriting it too early
+        // both groups' row sums, relative to the last block's maximum
         const uint32_t gl = g - 1u;
-        float* red_sum = red + ((gl + 1u) & 1u) * 2 * R;
-        red_sum[half * R + row] = l;
-        named_bar(bar_id, 64);
-        const float lt = l + red_sum[(half ^ 1) * R + row];
-        named_bar(bar_id, 64);
-        if (ok) ok = mbar_wait(&p_empty[gl & 1u], (gl >> 1) & 1u, status);
+        lrow[grp * R + row] = l;
+        mrow[grp * R + row] = m;
+        named_bar(pair_id, 64);
+        const float mf = mrow[(gl & 1u) * R + row];  // the group of the last block knows the final one
+        const float mz = mf == -INFINITY ? 0.f : mf;
+        float lt = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) lt += lrow[x * R + row] * whale_ex2(mrow[x * R + row] - mz);
+        named_bar(pair_id, 64);  // before the next unit overwrites them
+        if (ok) ok = mbar_wait(&p_empty[gl % C::NS], (gl / C::NS) & 1u, status);
         tc_fence_after();
         if (warp_on) {
           float vs = 1.f;  // V's reference exponent
@@ -567,7 +646,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           using S = SeqSlots<R, D>;
           float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
 #pragma unroll 1
-          for (int cc = half; cc < D / 32; cc += 2) {
+          for (int cc = grp; cc < D / 32; cc += 2) {
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
             tmem_ld_wait();
@@ -583,12 +662,12 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
               }
             }
           }
-          if (row_on && half == 0) {
+          if (row_on && grp == 0) {
             if (!whole) {
-              S::m(slot)[row] = m;
+              S::m(slot)[row] = mf;
               S::l(slot)[row] = lt;
             } else if (lse) {
-              lse[orow] = lt == 0.f ? -INFINITY : 0.69314718055994531f * ((m == -INFINITY ? 0.f : m) + log2f(lt));
+              lse[orow] = lt == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(lt));
             }
           }
         }
@@ -598,8 +677,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       } else if (row_on) {  // no key: nothing to attend to
         const uint32_t z[32] = {};
 #pragma unroll 1
-        for (int cc = half; cc < D / 32; cc += 2) whale_st_row32<T>(O + orow * D + cc * 32, z, 0.f, nullptr);
-        if (lse && half == 0) lse[orow] = -INFINITY;
+        for (int cc = grp; cc < D / 32; cc += 2) whale_st_row32<T>(O + orow * D + cc * 32, z, 0.f, nullptr);
+        if (lse && grp == 0) lse[orow] = -INFINITY;
       }
       __syncwarp();
       if (lane == 0) unit_done();
@@ -722,8 +801,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       };
       const uint8_t *kb = static_cast<const uint8_t*>(K8), *vb = static_cast<const uint8_t*>(V8);
       for (int j = u.j0; j < j1; ++j) {
-        if (j == u.j0) load(kb, a.k_exp, ref[0], j);
-        if (j + 1 < j1) load(kb, a.k_exp, ref[0], j + 1);
+        for (int k = u.j0; j == u.j0 && k < min(j1, u.j0 + C::AHEAD); ++k) load(kb, a.k_exp, ref[0], k);
+        if (j + C::AHEAD < j1) load(kb, a.k_exp, ref[0], j + C::AHEAD);
         load(vb, a.v_exp, ref[1], j);
       }
       __syncwarp();
