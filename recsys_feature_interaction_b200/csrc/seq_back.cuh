@@ -49,8 +49,11 @@ struct SbCfg {
   static constexpr int BARB = 512;
   static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
   static constexpr int REDB = 8 * 2 * 64 * 4;  // pair exchange of DQ; lse and delta of DKV's columns per warp, twice
-  static constexpr int FIXED = BARB + UNITB + REDB;
-  static constexpr int SBUF = D <= 128 ? 2 : 1;  // standing tiles in flight
+  static constexpr int STAGEB = 8 * SEQ_STAGE_BYTES;
+  static constexpr int FIXED = BARB + UNITB + REDB + STAGEB;
+  // Standing tiles in flight: two where units are short (DKV: as many blocks as query rows ask for),
+  // one where they are long and the room is better used for blocks that go by.
+  static constexpr int SBUF = DKV && D <= 128 ? 2 : 1;
   static constexpr int STAGES_RAW = (LIMIT - FIXED - 2 * SBUF * AB) / (2 * YBYTES);
   static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
   static constexpr int RAW = FIXED + 2 * SBUF * AB + STAGES * 2 * YBYTES;
@@ -336,6 +339,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const int bar_id = 1 + q;
     const float scale_log2 = a.scale * 1.4426950408889634f;
+    uint8_t* stage = reinterpret_cast<uint8_t*>(red) + C::REDB + (warp - 4) * SEQ_STAGE_BYTES;
     float* cols = red + (warp - 4) * 128;  // DKV: lse (base 2) [32] and delta [32] of this warp's columns, twice
     uint32_t g = 0, uc = 0;
     bool ok = true;
@@ -471,23 +475,21 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         tc_fence_after();
         ++uc;
         if (warp_on) {
+          const SeqRowsOut out(orow, row_on && ok);
           float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
 #pragma unroll 1
           for (int cc = half; cc < C::NACC * (D / 32); cc += 2) {
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::ACOL + cc * 32, o);
             tmem_ld_wait();
-            if (row_on && ok) {
-              if (whole) {
-                T* dst = (cc < D / 32 ? G1 : G2) + orow * D + (cc % (D / 32)) * 32;
-                whale_st_row32<T>(dst, o, 1.f, nullptr);
-              } else {
+            if (whole) {
+              seq_store_rows<D, T>(stage, o, 1.f, cc < D / 32 ? G1 : G2, (cc % (D / 32)) * 32, out);
+            } else if (row_on && ok) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
-                      make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
+                    make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
             }
           }
         }

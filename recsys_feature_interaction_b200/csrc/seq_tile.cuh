@@ -159,6 +159,48 @@ __device__ __forceinline__ float seq_max(const uint32_t (&v)[N]) {
   return seq_max2(seq_max3(a[0], a[1], a[2]), a[3]);
 }
 
+// Where a warp's 32 accumulator rows go: a lane stores 16 bytes of rows 8 k + lane / 4, k < 4.
+struct SeqRowsOut {
+  int64_t at[4];
+  bool on[4];
+  // row, on: this lane's own row of the output
+  __device__ __forceinline__ SeqRowsOut(int64_t row, bool valid) {
+    const uint32_t all = __ballot_sync(0xffffffffu, valid);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int from = 8 * k + (lane >> 2);
+      at[k] = __shfl_sync(0xffffffffu, row, from);
+      on[k] = (all >> from) & 1u;
+    }
+  }
+};
+constexpr int SEQ_STAGE_BYTES = 32 * 64;  // per warp
+
+// 32 columns of a warp's 32 rows, times scale, as T into out[row * D + col ..]: through a tile of the
+// warp's own in shared memory, so that a store covers 64 bytes of 8 rows and not 16 of 32 (which
+// keeps the load/store unit busy four times as long; it bounded the gradients of short sequences).
+template <int D, typename T>
+__device__ __forceinline__ void seq_store_rows(uint8_t* stage, const uint32_t (&o)[32], float scale, T* out, int col,
+                                               const SeqRowsOut& w) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = Half16<T>::pack2(__uint_as_float(o[8 * j + 2 * i]) * scale, __uint_as_float(o[8 * j + 2 * i + 1]) * scale);
+    *reinterpret_cast<uint4*>(stage + whale_swz<64>(lane, j)) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + whale_swz<64>(8 * k + (lane >> 2), lane & 3));
+    if (w.on[k]) *reinterpret_cast<uint4*>(out + w.at[k] * D + col + (lane & 3) * 8) = v;
+  }
+  __syncwarp();
+}
+
 template <int D_, int SRC_>
 struct StCfg {
   static constexpr int D = D_, SRC = SRC_;
@@ -175,12 +217,13 @@ struct StCfg {
   static constexpr int BARB = 512;                       // barriers, TMEM address, references
   static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
   static constexpr int REDB = 4 * R * 4;                 // what the softmax groups tell each other, per row
-  static constexpr int FIXED = BARB + UNITB + REDB;
-  static constexpr int QBUF = D <= 128 ? 2 : 1;          // Q tiles in flight: d = 160 has no room for two
-  static constexpr int STAGES_RAW = (LIMIT - FIXED - QBUF * TILEB) / TILEB;
+  static constexpr int STAGEB = 8 * SEQ_STAGE_BYTES;     // the softmax warps' output tiles
+  static constexpr int FIXED = BARB + UNITB + REDB + STAGEB;
+  // one Q tile: the next unit's is loaded once this one's last S is done, under its last blocks
+  static constexpr int STAGES_RAW = (LIMIT - FIXED - TILEB) / TILEB;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   // more than half an SM's shared memory: one block per SM, whose 512 TMEM columns are its own
-  static constexpr int RAW = FIXED + (QBUF + STAGES) * TILEB;
+  static constexpr int RAW = FIXED + (1 + STAGES) * TILEB;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
   // TMEM: NS buffers of S (P over their first 64 columns), then O. With three, S runs two blocks
   // ahead of P V, and a softmax group finds its next block ready; d = 160 has room for two.
@@ -190,7 +233,7 @@ struct StCfg {
   static constexpr int THREADS = SRC == SEQ_PAGED8 ? 512 : 384;
   static constexpr int LOADERS = 128;
   static_assert(OCOL + D <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
-  static_assert((2 * STAGES + 4 * NS + 2 + 2 * QBUF + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
+  static_assert((2 * STAGES + 4 * NS + 2 + 2 + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
 };
 
 // Key blocks [j0, j1) of a unit that hold keys (a unit without keys has a cost, but no block).
@@ -211,8 +254,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     if (threadIdx.x == 0) flag_error(a.status, kFlagBadShape);
     return;
   }
-  uint8_t* sQ = smem_raw;                              // [QBUF]
-  uint8_t* tiles = sQ + C::QBUF * C::TILEB;            // [STAGES]
+  uint8_t* sQ = smem_raw;
+  uint8_t* tiles = sQ + C::TILEB;                      // [STAGES]
   uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + C::STAGES * C::TILEB);
   uint64_t* kv_full = bars;                  // [STAGES] tile landed
   uint64_t* kv_empty = bars + C::STAGES;     // [STAGES] its product has read it
@@ -221,9 +264,9 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   uint64_t* p_empty = p_full + 2 * C::NS;    // [NS] P V has read it (so O holds that block)
   uint64_t* o_empty = p_empty + C::NS;       // O read by the softmax warps (per unit)
   uint64_t* fin = o_empty + 1;
-  uint64_t* q_full = fin + 1;                // [QBUF] the unit's Q rows landed
-  uint64_t* q_empty = q_full + C::QBUF;      // [QBUF] its last S has read them
-  uint64_t* u_full = q_empty + C::QBUF;      // [NU] unit handed over
+  uint64_t* q_full = fin + 1;                // the unit's Q rows landed
+  uint64_t* q_empty = q_full + 1;            // its last S has read them
+  uint64_t* u_full = q_empty + 1;            // [NU] unit handed over
   uint64_t* u_empty = u_full + C::NU;        // [NU] every role is done with it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + C::NU);
   int32_t* refs = reinterpret_cast<int32_t*>(tmem_slot + 4);  // [NU][2] exponent references of K and V
@@ -250,10 +293,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&p_empty[i], 1);
     }
-    for (int i = 0; i < C::QBUF; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(o_empty, 8);
     mbar_init(fin, 1);
     for (int i = 0; i < C::NU; ++i) {
@@ -314,25 +355,22 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     // ------------------------------------------------------------ producer
     // The whole warp walks, one thread issues. With a cache each lane holds one page of a window of
     // 32, one for K and one for V (K runs ahead), so that a tile does not wait for its table entries.
-    int s = 0, qs = 0;
+    int s = 0;
     uint32_t ph = 0, qph = 0;
     bool ok = true;
     SeqUnit u;
     const int tokens = a.tile / group;  // per Q tile: its rows are (token, head) with the head first
     auto load_q = [&]() -> bool {
-      if (!mbar_wait(&q_empty[qs], qph ^ 1u, status)) return false;
+      if (!mbar_wait(q_empty, qph ^ 1u, status)) return false;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&q_full[qs], static_cast<uint32_t>(a.tile * D * 2));
+        mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(a.tile * D * 2));
 #pragma unroll
         for (int bx = 0; bx < C::NBOX; ++bx)
-          tma_load_3d(&tmQ, &q_full[qs], sQ + qs * C::TILEB + bx * C::BOXB, bx * C::BW, u.h * group,
+          tma_load_3d(&tmQ, q_full, sQ + bx * C::BOXB, bx * C::BW, u.h * group,
                       static_cast<int32_t>(u.q_begin) + u.t * tokens);
       }
       __syncwarp();
-      if (++qs == C::QBUF) {
-        qs = 0;
-        qph ^= 1u;
-      }
+      qph ^= 1u;
       return true;
     };
     int win[2] = {-1, -1};    // the windows' numbers (page index / 32) and this lane's page of each
@@ -399,7 +437,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     }
     // copies already issued must land before the block exits (a failed wait left some behind)
     if (lane == 0 && status_set(status)) {
-      for (int i = 0; i < C::QBUF; ++i) mbar_drain(&q_full[i], qph ^ (i < qs ? 0u : 1u), status);
+      mbar_drain(q_full, qph ^ 1u, status);
       if (SRC != SEQ_PAGED8)
         for (int i = 0; i < C::STAGES; ++i) mbar_drain(&kv_full[i], ph ^ (i < s ? 0u : 1u), status);
     }
@@ -410,8 +448,8 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     const bool bf = Half16<T>::kBF16;
     const uint32_t idS = idesc_f16kind_f32(R, KB, 0, 0, bf);
     const uint32_t idO = idesc_f16kind_f32(R, D, 0, 1, bf);
-    int s = 0, qs = 0;
-    uint32_t ph = 0, qph = 0, g = 0, uc = 0;
+    int s = 0;
+    uint32_t ph = 0, g = 0, uc = 0;
     bool ok = true;
     SeqUnit u;
     auto step = [&]() {
@@ -425,7 +463,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       if (elect_one()) {
         tc_fence_after();
         const uint32_t k = seq_desc_lo(smem_u32(tiles + s * C::TILEB), 16);
-        const uint32_t qd = seq_desc_lo(smem_u32(sQ + qs * C::TILEB), 16);
+        const uint32_t qd = seq_desc_lo(smem_u32(sQ), 16);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t at = ((ks / (C::BW / 16)) * C::BOXB + (ks % (C::BW / 16)) * 32) >> 4;
@@ -433,7 +471,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         }
         umma_commit(&s_full[gb % C::NS]);
         umma_commit(&kv_empty[s]);
-        if (last) umma_commit(&q_empty[qs]);
+        if (last) umma_commit(q_empty);
       }
       __syncwarp();
       step();
@@ -478,7 +516,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     while (ok && unit_take(u)) {
       const int j1 = seq_real_end(a, u, group, a.tile, KB);
       if (u.j0 < j1) {
-        ok = mbar_wait(&q_full[qs], qph, status);
+        ok = mbar_wait(q_full, uc & 1u, status);
         for (int k = 0; ok && k < min(C::AHEAD, j1 - u.j0); ++k) ok = issue_s(g + k, u.j0 + k + 1 == j1);
         for (int j = u.j0; ok && j < j1; ++j) {
           if (j + C::AHEAD < j1) ok = issue_s(g + C::AHEAD, j + C::AHEAD + 1 == j1);
@@ -488,10 +526,6 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           ++g;
         }
         ++uc;
-        if (++qs == C::QBUF) {
-          qs = 0;
-          qph ^= 1u;
-        }
       }
       __syncwarp();
       if (lane == 0) unit_done();
@@ -516,6 +550,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     const int pair_id = 1 + q, hear_id = 6 + q + 4 * (grp ^ 1), tell_id = 6 + q + 4 * grp;
     float* mrow = red;           // [2][R] running maximum after a group's last block
     float* lrow = red + 2 * R;   // [2][R] row sums at the end of a unit, relative to mrow
+    uint8_t* stage = reinterpret_cast<uint8_t*>(red) + C::REDB + (warp - 4) * SEQ_STAGE_BYTES;
     uint32_t g = 0;
     // After a failed wait a thread stops waiting but walks the unit to its end, so that the
     // warp-collective TMEM accesses and the barriers stay converged; the pair of warps of a lane
@@ -643,6 +678,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
             vs = seq_ex2(static_cast<float>(refs[2 * (ui % C::NU) + 1] - 127));
           const float inv = whole ? (lt == 0.f ? 0.f : vs / lt) : vs;
+          const SeqRowsOut out(orow, row_on && ok);
           using S = SeqSlots<R, D>;
           float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
 #pragma unroll 1
@@ -650,16 +686,14 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
             tmem_ld_wait();
-            if (row_on && ok) {
-              if (whole) {
-                whale_st_row32<T>(O + orow * D + cc * 32, o, inv, nullptr);
-              } else {
+            if (whole) {
+              seq_store_rows<D, T>(stage, o, inv, O, cc * 32, out);
+            } else if (row_on && ok) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
-                      make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                  __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
-              }
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
+                    make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
             }
           }
           if (row_on && grp == 0) {
