@@ -305,49 +305,49 @@ __device__ __forceinline__ void seq_leave_note(float* ws, int64_t piece, const S
   *SeqSlots<R, D>::note(ws, piece) = n;
 }
 
-// Joins the pieces of cut units. blockIdx.x = piece * (R / CR) + block of CR rows. m and l of a row
+// Joins the pieces of cut units: a block does CR rows of the unit that piece blockIdx.x / (R / CR)
+// leaves unfinished, a thread 8 columns of a row. Bound by the latency of its loads (the note, then
+// the maxima, then the rest), so the loads of several pieces are in flight at once. m and l of a row
 // that a piece saw no key of are -inf and 0.
-constexpr int SEQ_COMBINE_THREADS = 128;
 template <int R, int CR, int D, typename T>
-__global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
+__global__ void __launch_bounds__(CR * D / 8)
     seq_combine_kernel(float* ws, T* __restrict__ O, float* __restrict__ lse, int32_t q_heads, int32_t pieces) {
   using S = SeqSlots<R, D>;
   const int32_t c = blockIdx.x / (R / CR);
-  const int first = (blockIdx.x % (R / CR)) * CR;
+  const int r = (blockIdx.x % (R / CR)) * CR + threadIdx.x % CR, d = (threadIdx.x / CR) * 8;
   cudaGridDependencySynchronize();
   const SeqNote n = *S::note(ws, c);
-  if (first >= n.rows) return;
-  for (int i = threadIdx.x; i < CR * (D / 8); i += SEQ_COMBINE_THREADS) {
-    const int r = first + i % CR, d = (i / CR) * 8;
-    if (r >= n.rows) continue;
-    float* s0 = S::slot(ws, pieces, c, false);
-    float m = S::m(s0)[r];
-    for (int k = 1; k < n.pieces; ++k) m = fmaxf(m, S::m(S::slot(ws, pieces, c + k, true))[r]);
-    const float mz = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < n.pieces; ++k) {
-      float* s = k == 0 ? s0 : S::slot(ws, pieces, c + k, true);
-      const float f = seq_ex2(S::m(s)[r] - mz);
-      const float4 x = *reinterpret_cast<const float4*>(S::o(s, r, d));
-      const float4 y = *reinterpret_cast<const float4*>(S::o(s, r, d + 4));
-      l += f * S::l(s)[r];
-      o[0] += f * x.x;
-      o[1] += f * x.y;
-      o[2] += f * x.z;
-      o[3] += f * x.w;
-      o[4] += f * y.x;
-      o[5] += f * y.y;
-      o[6] += f * y.z;
-      o[7] += f * y.w;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no piece saw a key
-    const int pr = n.r0 + r;
-    const int64_t row = (n.begin + pr / n.group) * q_heads + n.h * n.group + pr % n.group;
-    *reinterpret_cast<uint4*>(O + row * D + d) =
-        make_uint4(Half16<T>::pack2(o[0] * inv, o[1] * inv), Half16<T>::pack2(o[2] * inv, o[3] * inv),
-                   Half16<T>::pack2(o[4] * inv, o[5] * inv), Half16<T>::pack2(o[6] * inv, o[7] * inv));
-    if (lse && d == 0) lse[row] = l == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(l));
+  if (r >= n.rows) return;
+  // piece c left the unit's beginning in its second slot, the others what they entered in their first
+  auto slot = [&](int k) { return S::slot(ws, pieces, c + k, k != 0); };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int k = 0; k < n.pieces; ++k) m = fmaxf(m, S::m(slot(k))[r]);
+  const float mz = m == -INFINITY ? 0.f : m;
+  float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < n.pieces; ++k) {
+    float* s = slot(k);
+    const float f = seq_ex2(S::m(s)[r] - mz);
+    const float4 x = *reinterpret_cast<const float4*>(S::o(s, r, d));
+    const float4 y = *reinterpret_cast<const float4*>(S::o(s, r, d + 4));
+    l += f * S::l(s)[r];
+    o[0] += f * x.x;
+    o[1] += f * x.y;
+    o[2] += f * x.z;
+    o[3] += f * x.w;
+    o[4] += f * y.x;
+    o[5] += f * y.y;
+    o[6] += f * y.z;
+    o[7] += f * y.w;
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: no piece saw a key
+  const int pr = n.r0 + r;
+  const int64_t row = (n.begin + pr / n.group) * q_heads + n.h * n.group + pr % n.group;
+  *reinterpret_cast<uint4*>(O + row * D + d) =
+      make_uint4(Half16<T>::pack2(o[0] * inv, o[1] * inv), Half16<T>::pack2(o[2] * inv, o[3] * inv),
+                 Half16<T>::pack2(o[4] * inv, o[5] * inv), Half16<T>::pack2(o[6] * inv, o[7] * inv));
+  if (lse && d == 0) lse[row] = l == 0.f ? -INFINITY : 0.69314718055994531f * (mz + log2f(l));
 }
 
 }  // namespace wk

@@ -515,40 +515,37 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
   }
 }
 
-// Adds the pieces of cut units, in the order of the pieces. blockIdx.x = piece * (128 / CR) + block
-// of CR rows; the first D columns go to G1, the others to G2.
+// Adds the pieces of cut units, in the order of the pieces (as seq_combine_kernel); the first D
+// columns go to G1, the others to G2.
 template <int CR, int D, int NACC, typename T>
-__global__ void __launch_bounds__(SEQ_COMBINE_THREADS)
+__global__ void __launch_bounds__(CR * NACC * D / 8)
     seq_sum_kernel(float* ws, T* __restrict__ G1, T* __restrict__ G2, int32_t heads, int32_t pieces) {
   using S = SeqSlots<128, NACC * D>;
   const int32_t c = blockIdx.x / (128 / CR);
-  const int first = (blockIdx.x % (128 / CR)) * CR;
+  const int r = (blockIdx.x % (128 / CR)) * CR + threadIdx.x % CR, d = (threadIdx.x / CR) * 8;
   cudaGridDependencySynchronize();
   const SeqNote n = *S::note(ws, c);
-  if (first >= n.rows) return;
-  for (int i = threadIdx.x; i < CR * (NACC * D / 8); i += SEQ_COMBINE_THREADS) {
-    const int r = first + i % CR, d = (i / CR) * 8;
-    if (r >= n.rows) continue;
-    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < n.pieces; ++k) {
-      float* s = S::slot(ws, pieces, c + k, k != 0);
-      const float4 x = *reinterpret_cast<const float4*>(S::o(s, r, d));
-      const float4 y = *reinterpret_cast<const float4*>(S::o(s, r, d + 4));
-      o[0] += x.x;
-      o[1] += x.y;
-      o[2] += x.z;
-      o[3] += x.w;
-      o[4] += y.x;
-      o[5] += y.y;
-      o[6] += y.z;
-      o[7] += y.w;
-    }
-    const int pr = n.r0 + r;
-    const int64_t row = (n.begin + pr / n.group) * heads + n.h * n.group + pr % n.group;
-    T* dst = (d < D ? G1 : G2) + row * D + d % D;
-    *reinterpret_cast<uint4*>(dst) = make_uint4(Half16<T>::pack2(o[0], o[1]), Half16<T>::pack2(o[2], o[3]),
-                                                Half16<T>::pack2(o[4], o[5]), Half16<T>::pack2(o[6], o[7]));
+  if (r >= n.rows) return;
+  float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < n.pieces; ++k) {
+    float* s = S::slot(ws, pieces, c + k, k != 0);
+    const float4 x = *reinterpret_cast<const float4*>(S::o(s, r, d));
+    const float4 y = *reinterpret_cast<const float4*>(S::o(s, r, d + 4));
+    o[0] += x.x;
+    o[1] += x.y;
+    o[2] += x.z;
+    o[3] += x.w;
+    o[4] += y.x;
+    o[5] += y.y;
+    o[6] += y.z;
+    o[7] += y.w;
   }
+  const int pr = n.r0 + r;
+  const int64_t row = (n.begin + pr / n.group) * heads + n.h * n.group + pr % n.group;
+  T* dst = (d < D ? G1 : G2) + row * D + d % D;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(Half16<T>::pack2(o[0], o[1]), Half16<T>::pack2(o[2], o[3]),
+                                              Half16<T>::pack2(o[4], o[5]), Half16<T>::pack2(o[6], o[7]));
 }
 
 // Zeros in the rows between a sequence's last key and the next sequence (padded batches).

@@ -12,11 +12,13 @@
 // for 4 real ones), and P^T goes from accumulator to operand layout by two movmatrix. Softmax
 // statistics are kept per warp and joined over the block's warps, and over blocks, at the end.
 //
-// 8-bit rows: e4m3 bits shifted into a 16-bit float's fields are the value times a fixed power of
-// two (2^-8 in fp16, 2^-120 in bf16), so a conversion is a shift, a mask and a multiplication by a
-// power of two, exact. K's exponent joins the fp32 score; V's joins the conversion, relative to a
-// reference that is raised (and O rescaled) when a row is more than 2^7 above it, so that fp16
-// holds every row down to 2^-15 of the largest exactly.
+// 8-bit rows are converted to fp16, whatever the type of Q and O: e4m3 values are exact in it, and
+// one instruction converts two. The rows' powers of two stay apart: K's joins the fp32 score, V's
+// is multiplied onto the converted pair, relative to a reference that is raised (and O rescaled) when
+// a row is more than 2^7 above it, so that every row down to 2^-15 of the largest enters exactly.
+// bf16 queries are scaled by a power of two of their own row, so that they are exact in fp16 down to
+// 2^-39 of the row's largest. (Shifting e4m3's bits into bf16's fields took four instructions a pair
+// and made the kernel wait for the ALU: 86 us at 64 sequences of up to 15,000 keys.)
 #pragma once
 
 #include "seq_args.cuh"
@@ -62,6 +64,20 @@ __device__ __forceinline__ uint32_t seq_raw2(uint32_t w) {
 template <typename T>
 constexpr int kRawPow = Half16<T>::kBF16 ? 120 : 8;
 
+// Two e4m3 values as two fp16 values.
+__device__ __forceinline__ uint32_t seq_e4m3_f16(uint16_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));
+  return r;
+}
+__device__ __forceinline__ uint16_t seq_lo16(uint32_t w) { return static_cast<uint16_t>(w); }
+__device__ __forceinline__ uint16_t seq_hi16(uint32_t w) { return static_cast<uint16_t>(w >> 16); }
+
+// 2^dx in fp16 (dx <= 15), bits; 0 below its range.
+__device__ __forceinline__ uint32_t seq_pow_f16(int dx) {
+  return dx >= -14 ? static_cast<uint32_t>(dx + 15) << 10 : (dx >= -24 ? 1u << (dx + 24) : 0u);
+}
+
 // 8x8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t seq_movmatrix(uint32_t x) {
   uint32_t r;
@@ -104,6 +120,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     seq_rows_kernel(const T* __restrict__ Q, const void* __restrict__ K, const void* __restrict__ V, T* __restrict__ O,
                     float* __restrict__ lse, float* __restrict__ ws, SeqArgs a, int64_t pieces) {
   using C = SrCfg<D, SRC>;
+  using CT = std::conditional_t<C::Q8, __half, T>;  // the tensor cores' operand type
   constexpr int R = 8 * NQ;
   constexpr int PITCH = D + 4;
   __shared__ int64_t sh[SEQ_ROWS_THREADS / 32 + 4];
@@ -123,6 +140,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     const int r0 = u.t * R;
     // Q^T as the B operand: column g of block q is packed row r0 + 8 q + g
     uint32_t qf[NQ][C::KSTEPS][2];
+    float qpow[NQ][2];  // powers of two taken out of the thread's rows (bf16 queries, 8-bit keys)
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
       const int r = r0 + 8 * q + g;
@@ -132,17 +150,35 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
       for (int s = 0; s < C::KSTEPS; ++s) {
         uint2 v = make_uint2(0u, 0u);
         if (on) v = *reinterpret_cast<const uint2*>(src + C::kd(s, c));
-        if constexpr (C::Q8) {  // the order of the bytes of a K word: (0, 2), (1, 3)
-          qf[q][s][0] = __byte_perm(v.x, v.y, 0x5410);
-          qf[q][s][1] = __byte_perm(v.x, v.y, 0x7632);
-        } else {
-          qf[q][s][0] = v.x;
-          qf[q][s][1] = v.y;
-        }
+        qf[q][s][0] = v.x;
+        qf[q][s][1] = v.y;
+      }
+      qpow[q][0] = qpow[q][1] = 1.f;
+      if constexpr (C::Q8 && Half16<T>::kBF16) {
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < C::KSTEPS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[q][s][i])), fabsf(bf16_hi(qf[q][s][i]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // top = 1.f * 2^(e - 127): times 2^(141 - e) it lies in [2^14, 2^15)
+        const int e = static_cast<int>(__float_as_uint(top) >> 23);
+        const bool plain = e < 15 || e > 254;  // nothing to scale, or not finite
+        const float f = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        const float back = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+        for (int s = 0; s < C::KSTEPS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qf[q][s][i] = Half16<__half>::pack2(bf16_lo(qf[q][s][i]) * f, bf16_hi(qf[q][s][i]) * f);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) qpow[q][x] = __shfl_sync(0xffffffffu, back, (2 * c + x) * 4);
       }
     }
     // keys that the thread's rows (r0 + 8 q + 2 c, + 1) see
-    int seen[NQ][2], most = 0;
+    int seen[NQ][2], most = 0, least = INT32_MAX;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -150,9 +186,13 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
         const int r = r0 + 8 * q + 2 * c + e;
         seen[q][e] = r < u.rows ? seq_seen(u.len, u.n, r / group, a.causal) : 0;
         most = max(most, seen[q][e]);
+        if (r < u.rows) least = min(least, seen[q][e]);
       }
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
     most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+    least = min(least, most);
     const int kend = min(most, u.j1 * C::KB);
     float m[NQ][2], l[NQ][2], acc[NQ][C::DT][4];
     int vref = -1000;  // reference exponent of V; set by the first step
@@ -169,63 +209,58 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     uint32_t kr[C::KS / 8][C::KCH * C::KCB / 4];
     uint32_t vr[C::KS / 4][C::VL / 4];
     uint32_t ke[C::KS / 8], ve[C::KS / 4];
-    int32_t page[C::KS / 16], npage[C::KS / 16];
+    // a step's keys in groups of 16, each within one page: the group's first row (of the tensor or the
+    // cache), or -1 where there is nothing to load
+    int64_t at[C::KS / 16];
     const int32_t* trow = SRC ? a.table + static_cast<int64_t>(u.b) * a.table_width : nullptr;
     const int pmask = (1 << a.page_shift) - 1;
-
-    auto pages = [&](int k0, int32_t (&p)[C::KS / 16]) {  // the pages of a step's keys
-      if constexpr (SRC != SEQ_JAGGED) {
+    auto place_of = [&](int k0, int64_t (&p)[C::KS / 16]) {
 #pragma unroll
-        for (int i = 0; i < C::KS / 16; ++i) {
-          p[i] = -1;
-          if (k0 + 16 * i < kend) {
-            p[i] = seq_page(trow, k0 + 16 * i, a.page_shift, a.num_pages);
-            if (p[i] < 0) flag_error(a.status, kFlagBadShape);
+      for (int i = 0; i < C::KS / 16; ++i) {
+        const int k = k0 + 16 * i;
+        p[i] = -1;
+        if (k < kend) {
+          if constexpr (SRC == SEQ_JAGGED) {
+            p[i] = u.kv_begin + k;
+          } else {
+            const int page = seq_page(trow, k, a.page_shift, a.num_pages);
+            if (page < 0) flag_error(a.status, kFlagBadShape);
+            else p[i] = ((static_cast<int64_t>(page) * a.kv_heads + u.h) << a.page_shift) + (k & pmask);
           }
         }
       }
     };
-    // row index (of the tensor or the cache) of key k, whose page is p; -1: nothing to load
-    auto row_of = [&](int k, int32_t p) -> int64_t {
-      if (k >= kend) return -1;
-      if constexpr (SRC == SEQ_JAGGED) return u.kv_begin + k;
-      if (p < 0) return -1;
-      return ((static_cast<int64_t>(p) * a.kv_heads + u.h) << a.page_shift) + (k & pmask);
-    };
-    auto load_k = [&](int k0) {
+    const int64_t k_row = SRC == SEQ_JAGGED ? a.k_stride * 2 : D * C::ES, v_row = SRC == SEQ_JAGGED ? a.v_stride * 2 : D * C::ES;
+    const char* k_lane = static_cast<const char*>(K) + (SRC == SEQ_JAGGED ? u.h * D * 2 : 0) + g * k_row + c * C::KCB;
+    const char* v_lane = static_cast<const char*>(V) + (SRC == SEQ_JAGGED ? u.h * D * 2 : 0) + 2 * c * v_row + g * C::VCB;
+    // K rows g and g + 8 of each group; all: the step's keys are all there
+    auto load_k = [&](int k0, bool all) {
 #pragma unroll
       for (int i = 0; i < C::KS / 8; ++i) {
-        const int64_t row = row_of(k0 + 8 * i + g, SRC ? page[i / 2] : 0);
+        const int r = 8 * (i & 1);
         ke[i] = 0;
-        if (row >= 0) {
-          const char* p = SRC == SEQ_JAGGED
-                              ? static_cast<const char*>(K) + (row * a.k_stride + u.h * D) * 2
-                              : static_cast<const char*>(K) + row * (D * C::ES);
+        if (at[i / 2] >= 0 && (all || k0 + 16 * (i / 2) + r + g < kend)) {
+          const char* p = k_lane + (at[i / 2] + r) * k_row;
 #pragma unroll
-          for (int x = 0; x < C::KCH; ++x)
-            seq_ldg<C::KCB>(p + (x * 4 + c) * C::KCB, &kr[i][x * (C::KCB / 4)]);
-          if constexpr (C::Q8) ke[i] = __ldg(a.k_exp + row);
+          for (int x = 0; x < C::KCH; ++x) seq_ldg<C::KCB>(p + x * 4 * C::KCB, &kr[i][x * (C::KCB / 4)]);
+          if constexpr (C::Q8) ke[i] = __ldg(a.k_exp + at[i / 2] + r + g);
         } else {
 #pragma unroll
           for (int x = 0; x < C::KCH * C::KCB / 4; ++x) kr[i][x] = 0u;
         }
       }
     };
-    // V rows of keys 16 s + 2 c, + 1, + 8, + 9
-    auto load_v = [&](int k0) {
+    // V rows 2 c, + 1, + 8, + 9 of each group
+    auto load_v = [&](int k0, bool all) {
 #pragma unroll
       for (int i = 0; i < C::KS / 4; ++i) {
-        const int k = k0 + 16 * (i / 4) + 2 * c + (i & 1) + 8 * ((i >> 1) & 1);
-        const int64_t row = row_of(k, SRC ? page[i / 4] : 0);
+        const int r = (i & 1) + 8 * ((i >> 1) & 1);
         ve[i] = 0;
-        if (row >= 0) {
-          const char* p = SRC == SEQ_JAGGED
-                              ? static_cast<const char*>(V) + (row * a.v_stride + u.h * D) * 2
-                              : static_cast<const char*>(V) + row * (D * C::ES);
+        if (at[i / 4] >= 0 && (all || k0 + 16 * (i / 4) + r + 2 * c < kend)) {
+          const char* p = v_lane + (at[i / 4] + r) * v_row;
 #pragma unroll
-          for (int x = 0; x < C::VCH; ++x)
-            seq_ldg<C::VCB>(p + (x * 8 + g) * C::VCB, &vr[i][x * (C::VCB / 4)]);
-          if constexpr (C::Q8) ve[i] = __ldg(a.v_exp + row);
+          for (int x = 0; x < C::VCH; ++x) seq_ldg<C::VCB>(p + x * 8 * C::VCB, &vr[i][x * (C::VCB / 4)]);
+          if constexpr (C::Q8) ve[i] = __ldg(a.v_exp + at[i / 4] + r + 2 * c);
         } else {
 #pragma unroll
           for (int x = 0; x < C::VL / 4; ++x) vr[i][x] = 0u;
@@ -235,14 +270,14 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
     // steps of this warp: block steps j0 .. j1, SUB each
     const int steps = (u.j1 - u.j0) * C::SUB;
     auto key_of = [&](int i) { return (u.j0 + i / C::SUB) * C::KB + ((i % C::SUB) * SEQ_ROWS_WARPS + warp) * C::KS; };
-    pages(key_of(0), page);
-    load_k(key_of(0));
-    load_v(key_of(0));
+    place_of(key_of(0), at);
+    load_k(key_of(0), false);
+    load_v(key_of(0), false);
     for (int i = 0; i < steps; ++i) {
       const int k0 = key_of(i);
       if (k0 >= kend) break;  // a warp's later steps lie behind the end too
       const int k1 = i + 1 < steps ? key_of(i + 1) : kend;
-      pages(k1, npage);
+      place_of(k1, at);  // this step's V is in registers already
       // S^T
       float s[NQ][C::KS / 16][4];
 #pragma unroll
@@ -258,17 +293,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
           uint32_t a0, a1, a2, a3;
           if constexpr (C::Q8) {
             const uint32_t x = kr[2 * t][ks], y = kr[2 * t + 1][ks];
-            a0 = seq_raw2<T>(x << 8);
-            a1 = seq_raw2<T>(y << 8);
-            a2 = seq_raw2<T>(x);
-            a3 = seq_raw2<T>(y);
-            if constexpr (Half16<T>::kBF16) {  // out of the range where products would underflow
-              constexpr uint32_t f = 0x7B807B80u;  // 2^120 twice
-              a0 = seq_mul2<T>(a0, f);
-              a1 = seq_mul2<T>(a1, f);
-              a2 = seq_mul2<T>(a2, f);
-              a3 = seq_mul2<T>(a3, f);
-            }
+            a0 = seq_e4m3_f16(seq_lo16(x));
+            a1 = seq_e4m3_f16(seq_lo16(y));
+            a2 = seq_e4m3_f16(seq_hi16(x));
+            a3 = seq_e4m3_f16(seq_hi16(y));
           } else {
             a0 = kr[2 * t][2 * ks];
             a1 = kr[2 * t + 1][2 * ks];
@@ -276,44 +304,92 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
             a3 = kr[2 * t + 1][2 * ks + 1];
           }
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) mma_16816<T>(s[q][t], a0, a1, a2, a3, qf[q][ks][0], qf[q][ks][1]);
+          for (int q = 0; q < NQ; ++q) mma_16816<CT>(s[q][t], a0, a1, a2, a3, qf[q][ks][0], qf[q][ks][1]);
         }
       // factors of the scores: the scale, and the rows' exponents
       float kf[C::KS / 8];
 #pragma unroll
       for (int t = 0; t < C::KS / 8; ++t) {
         kf[t] = scale_log2;
-        if constexpr (C::Q8) kf[t] *= seq_pow(ke[t]) * (Half16<T>::kBF16 ? 1.f : 256.f);
+        if constexpr (C::Q8) kf[t] *= seq_pow(ke[t]);
       }
-      // V of this step is in registers: its pages are not needed any more
+      const bool all1 = k1 + C::KS <= kend;
+      if (all1) load_k(k1, true);
+      else if (k1 < kend) load_k(k1, false);
+      // scores, and each thread's own maxima of its two columns
+      bool up = false;
+      float mx[NQ][2];
+      if (k0 + C::KS <= least) {
 #pragma unroll
-      for (int t = 0; t < C::KS / 16; ++t) page[t] = npage[t];
-      if (k1 < kend) load_k(k1);
-      // softmax weights
-      uint32_t pb[NQ][C::KS / 16][2];
-      bool raise = false;
-      float fac[NQ][2];
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        float mx[2] = {-INFINITY, -INFINITY};
+          for (int t = 0; t < C::KS / 16; ++t)
 #pragma unroll
-        for (int t = 0; t < C::KS / 16; ++t)
+            for (int e = 0; e < 4; ++e) s[q][t][e] *= kf[2 * t + (e >> 1)] * qpow[q][e & 1];
+      } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = k0 + 16 * t + 8 * (e >> 1) + g;
-            s[q][t][e] = k < seen[q][e & 1] ? s[q][t][e] * kf[2 * t + (e >> 1)] : -INFINITY;
-            mx[e & 1] = fmaxf(mx[e & 1], s[q][t][e]);
-          }
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int t = 0; t < C::KS / 16; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = k0 + 16 * t + 8 * (e >> 1) + g;
+              s[q][t][e] = k < seen[q][e & 1] ? s[q][t][e] * (kf[2 * t + (e >> 1)] * qpow[q][e & 1]) : -INFINITY;
+            }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          mx[q][e] = -INFINITY;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-          const float mn = fmaxf(m[q][e], mx[e]);
-          raise |= mn > m[q][e];
-          fac[q][e] = m[q][e] == -INFINITY ? 0.f : seq_ex2(m[q][e] - mn);
-          m[q][e] = mn;
-          l[q][e] *= fac[q][e];
+          for (int t = 0; t < C::KS / 16; ++t) mx[q][e] = fmaxf(mx[q][e], fmaxf(s[q][t][e], s[q][t][e + 2]));
+          up |= mx[q][e] > m[q][e] + 8.f;
         }
+      int top = -1000;
+      if constexpr (C::Q8) {
+#pragma unroll
+        for (int t = 0; t < C::KS / 4; ++t) top = max(top, ve[t] == 255 ? -1000 : static_cast<int>(ve[t]));
+        up |= top > vref + 7;
+      }
+      // The running maximum (and V's reference) moves only when a score is more than 2^8 above it (a
+      // row's exponent more than 2^7): one vote, and a reduction over the lanes only then.
+      if (__any_sync(0xffffffffu, up)) {
+        float vf = 1.f;
+        if constexpr (C::Q8) {
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          if (top > vref + 7) {  // uniform over the warp
+            vf = vref == -1000 ? 0.f : seq_ex2(static_cast<float>(vref - top));
+            vref = top;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          float fac[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx[q][e] = fmaxf(mx[q][e], __shfl_xor_sync(0xffffffffu, mx[q][e], o));
+            const float mn = fmaxf(m[q][e], mx[q][e]);
+            fac[e] = m[q][e] == -INFINITY ? 0.f : seq_ex2(m[q][e] - mn);
+            m[q][e] = mn;
+            l[q][e] *= fac[e];
+            fac[e] *= vf;
+          }
+#pragma unroll
+          for (int t = 0; t < C::DT; ++t) {
+            acc[q][t][0] *= fac[0];
+            acc[q][t][1] *= fac[1];
+            acc[q][t][2] *= fac[0];
+            acc[q][t][3] *= fac[1];
+          }
+        }
+      }
+      // softmax weights
+      uint32_t pb[NQ][C::KS / 16][2];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
         const float mz[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0], m[q][1] == -INFINITY ? 0.f : m[q][1]};
 #pragma unroll
         for (int t = 0; t < C::KS / 16; ++t) {
@@ -323,46 +399,19 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
             p[e] = seq_ex2(s[q][t][e] - mz[e & 1]);
             l[q][e & 1] += p[e];
           }
-          pb[q][t][0] = seq_movmatrix(Half16<T>::pack2(p[0], p[1]));
-          pb[q][t][1] = seq_movmatrix(Half16<T>::pack2(p[2], p[3]));
+          pb[q][t][0] = seq_movmatrix(Half16<CT>::pack2(p[0], p[1]));
+          pb[q][t][1] = seq_movmatrix(Half16<CT>::pack2(p[2], p[3]));
         }
       }
-      float vf = 1.f;  // change of V's reference
       uint32_t vfac[C::KS / 8];
       if constexpr (C::Q8) {
-        int top = -1000;
-#pragma unroll
-        for (int t = 0; t < C::KS / 4; ++t) top = max(top, ve[t] == 255 ? -1000 : static_cast<int>(ve[t]));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if (top > vref + 7) {  // uniform over the warp
-          vf = vref == -1000 ? 0.f : exp2f(static_cast<float>(vref - top));
-          vref = top;
-          raise = true;
-        }
 #pragma unroll
         for (int t = 0; t < C::KS / 8; ++t) {
-          float f[2];
+          uint32_t f[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int x = static_cast<int>(ve[2 * t + e]);
-            f[e] = x == 255 ? __uint_as_float(0x7FC00000u)
-                            : seq_ex2(static_cast<float>(max(x - vref, -140) + kRawPow<T>));
-          }
-          vfac[t] = Half16<T>::pack2(f[0], f[1]);
-        }
-      }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const float f0 = fac[q][0] * vf, f1 = fac[q][1] * vf;
-#pragma unroll
-          for (int t = 0; t < C::DT; ++t) {
-            acc[q][t][0] *= f0;
-            acc[q][t][1] *= f1;
-            acc[q][t][2] *= f0;
-            acc[q][t][3] *= f1;
-          }
+          for (int e = 0; e < 2; ++e)
+            f[e] = ve[2 * t + e] == 255 ? 0x7E00u : seq_pow_f16(static_cast<int>(ve[2 * t + e]) - vref);
+          vfac[t] = f[0] | (f[1] << 16);
         }
       }
       // O^T += V^T P^T
@@ -375,10 +424,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
           for (int h = 0; h < 2; ++h) {  // keys 2 c, + 1, then + 8, + 9
             if constexpr (C::Q8) {
               const int e = 2 * dt, wd = e / 4;  // elements e, e + 1: bytes of word wd
-              const uint32_t x = vr[4 * t + 2 * h][wd], y = vr[4 * t + 2 * h + 1][wd];
-              // bytes 1 and 3 of the result: the same byte of both keys' words
-              f[2 * h] = seq_mul2<T>(seq_raw2<T>(__byte_perm(x, y, (e % 4) ? 0x6020 : 0x4000)), vfac[2 * t + h]);
-              f[2 * h + 1] = seq_mul2<T>(seq_raw2<T>(__byte_perm(x, y, (e % 4) ? 0x7030 : 0x5010)), vfac[2 * t + h]);
+              // byte e of both keys, then byte e + 1 of both
+              const uint32_t w = __byte_perm(vr[4 * t + 2 * h][wd], vr[4 * t + 2 * h + 1][wd], (e % 4) ? 0x7362 : 0x5140);
+              f[2 * h] = seq_mul2<__half>(seq_e4m3_f16(seq_lo16(w)), vfac[2 * t + h]);
+              f[2 * h + 1] = seq_mul2<__half>(seq_e4m3_f16(seq_hi16(w)), vfac[2 * t + h]);
             } else {
               const uint32_t x = vr[4 * t + 2 * h][dt], y = vr[4 * t + 2 * h + 1][dt];
               f[2 * h] = __byte_perm(x, y, 0x5410);
@@ -386,9 +435,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
             }
           }
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) mma_16816<T>(acc[q][dt], f[0], f[1], f[2], f[3], pb[q][t][0], pb[q][t][1]);
+          for (int q = 0; q < NQ; ++q) mma_16816<CT>(acc[q][dt], f[0], f[1], f[2], f[3], pb[q][t][0], pb[q][t][1]);
         }
-      if (k1 < kend) load_v(k1);
+      if (all1) load_v(k1, true);
+      else if (k1 < kend) load_v(k1, false);
     }
 
     // the row sums over the lanes of a column, then the block's warps together

@@ -158,8 +158,8 @@ wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* 
   const wk_status s = launch(seq_rows_kernel<D, T, SRC, NQ>, pieces, SEQ_ROWS_THREADS, 0, st, static_cast<const T*>(Q), K,
                              V, static_cast<T*>(O), lse, a.uncut ? nullptr : ws, a, pieces);
   if (s != WK_OK || a.uncut) return s;
-  return launch(seq_combine_kernel<8 * NQ, 8 * NQ, D, T>, pieces, SEQ_COMBINE_THREADS, 0, st, ws, static_cast<T*>(O),
-                lse, a.q_heads, pieces);
+  return launch(seq_combine_kernel<8 * NQ, 8 * NQ, D, T>, pieces, NQ * D, 0, st, ws, static_cast<T*>(O), lse,
+                a.q_heads, pieces);
 }
 
 // ---- the tile kernel: any number of rows, 128 packed rows per tile (seq_tile.cuh)
@@ -217,8 +217,8 @@ wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* 
              int64_t{kSMs});
   if (s != WK_OK || a.uncut) return s;
   constexpr int CR = 16;
-  return launch(seq_combine_kernel<128, CR, D, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, 0, st, ws,
-                static_cast<T*>(O), lse, a.q_heads, int32_t{kSMs});
+  return launch(seq_combine_kernel<128, CR, D, T>, kSMs * (128 / CR), CR * D / 8, 0, st, ws, static_cast<T*>(O), lse,
+                a.q_heads, int32_t{kSMs});
 }
 
 int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : tile_ws(a, d); }
@@ -293,8 +293,8 @@ struct RunBackward {
                static_cast<const T*>(dO), lse, delta, static_cast<T*>(G1), static_cast<T*>(G2),
                x.uncut ? nullptr : slots, x, int64_t{kSMs});
     if (s != WK_OK || x.uncut) return s;
-    constexpr int CR = 16;
-    return launch(seq_sum_kernel<CR, D, C::NACC, T>, kSMs * (128 / CR), SEQ_COMBINE_THREADS, 0, st, slots,
+    constexpr int CR = 16 / C::NACC;
+    return launch(seq_sum_kernel<CR, D, C::NACC, T>, kSMs * (128 / CR), CR * C::NACC * D / 8, 0, st, slots,
                   static_cast<T*>(G1), static_cast<T*>(G2), DKV ? a.kv_heads : a.q_heads, int32_t{kSMs});
   }
 
