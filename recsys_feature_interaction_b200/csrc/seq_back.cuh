@@ -15,8 +15,8 @@
 // Both operands of T1, T2 come from shared memory, the tiles that go by are read a second time as
 // MN-major operands of the accumulating products, whose A operands (P, dS) are written over the
 // columns of T1, T2 that the same thread has just read, so the element-wise warps (two per lane
-// quarter, 32 columns each) need no barrier among themselves. T1, T2 are double-buffered where TMEM
-// has room beside the accumulators (512 columns: not for dK and dV of d = 160).
+// quarter, 32 columns each) need no barrier among themselves. T1 and T2 of the next block are
+// computed under this one's element-wise work as far as TMEM has room beside the accumulators.
 //
 // delta comes from the stored (rounded) O, except where one block holds all keys of a row: there it
 // is sum P dP in fp32. With few keys dP - delta cancels almost wholly (with one key it is 0), and
@@ -58,8 +58,13 @@ struct SbCfg {
   static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
   static constexpr int RAW = FIXED + 2 * SBUF * AB + STAGES * 2 * YBYTES;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;  // one block per SM: its TMEM is its own
-  static constexpr int TB = 256 + NACC * D <= 512 ? 2 : 1;
-  static constexpr int ACOL = TB * 128;  // TMEM: T1, T2 of each buffer, then the accumulators
+  // TMEM: SLOTS places of 64 columns that T1 and T2 of the blocks take in turn, then the accumulators.
+  // With four, both of the next block are computed under this one's element-wise work; with three
+  // (dK and dV of d = 160) its T1 is.
+  static constexpr int SLOTS = 256 + NACC * D <= 512 ? 4 : 3;
+  static constexpr int ACOL = SLOTS * 64;
+  static __device__ __forceinline__ uint32_t t1(uint32_t g) { return (2u * g) % SLOTS * 64u; }
+  static __device__ __forceinline__ uint32_t t2(uint32_t g) { return (2u * g + 1u) % SLOTS * 64u; }
   static constexpr int THREADS = 384;
   static_assert(ACOL + NACC * D <= 512 && STAGES >= 2 && AB % 1024 == 0 && YBYTES % 1024 == 0, "layout");
   static_assert((2 * SBUF + 2 * STAGES + 7 + 2 * NU) * 8 + 8 <= BARB, "barriers");
@@ -232,8 +237,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    // T of block t + TB is written over the buffer that P and dS of block t were read from; the
-    // MMAs of a thread run in issue order, so it only has to be issued after them.
+    // T1 and T2 are written over places that P and dS of earlier blocks were read from; the MMAs of a
+    // thread run in issue order, so they only have to be issued after those.
     const bool bf = Half16<T>::kBF16;
     const uint32_t idT = idesc_f16kind_f32(C::R, C::YB, 0, 0, bf);
     const uint32_t idA = idesc_f16kind_f32(C::R, D, 0, 1, bf);
@@ -241,54 +246,55 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     uint32_t tph = 0, aph = 0, g = 0, uc = 0;
     bool ok = true;
     SeqUnit u;
-    auto issue_t = [&](int j, uint32_t gb) -> bool {
-      if (!mbar_wait(&y_full[ts], tph, status)) return false;
-      const int valid = min(a.block, passing(u) - j * a.block);
-      if (valid < C::YB) {
-        constexpr int UR = C::SWB / 16;  // 16-byte units of a box row
-        for (int i = lane; i < (C::YB - valid) * 2 * C::NBOX * UR; i += 32) {
-          const int r = valid + i / (2 * C::NBOX * UR), x = i % (2 * C::NBOX * UR);
-          *reinterpret_cast<uint4*>(sY + 2 * ts * C::YBYTES + (x / UR) * C::YBOXB + r * C::SWB + (x % UR) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+    // the block in ring place ts: T1 (w = 0, the first to need it) and T2 (w = 1, the last)
+    auto issue_t = [&](int w, int j, uint32_t gb) -> bool {
+      if (w == 0) {
+        if (!mbar_wait(&y_full[ts], tph, status)) return false;
+        const int valid = min(a.block, passing(u) - j * a.block);
+        if (valid < C::YB) {
+          constexpr int UR = C::SWB / 16;  // 16-byte units of a box row
+          for (int i = lane; i < (C::YB - valid) * 2 * C::NBOX * UR; i += 32) {
+            const int r = valid + i / (2 * C::NBOX * UR), x = i % (2 * C::NBOX * UR);
+            *reinterpret_cast<uint4*>(sY + 2 * ts * C::YBYTES + (x / UR) * C::YBOXB + r * C::SWB + (x % UR) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
       }
       if (elect_one()) {
         tc_fence_after();
-        const uint32_t x = seq_desc_lo(smem_u32(sA + 2 * sb * C::AB), 16);
-        const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * ts * C::YBYTES), 16);
-        const uint32_t t1 = tmem + (gb % C::TB) * 128;
+        const uint32_t x = seq_desc_lo(smem_u32(sA + (2 * sb + w) * C::AB), 16);
+        const uint32_t y = seq_desc_lo(smem_u32(sY + (2 * ts + w) * C::YBYTES), 16);
+        const uint32_t t = tmem + (w ? C::t2(gb) : C::t1(gb));
 #pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
-            seq_mma_ss<C::DESC_HI>(t1 + w * 64, x + ((w * C::AB + bx * C::ABOXB + kin * 32) >> 4),
-                                   y + ((w * C::YBYTES + bx * C::YBOXB + kin * 32) >> 4), idT, ks != 0 ? 1u : 0u);
-          }
-        umma_commit(&t_full[gb % C::TB]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int bx = ks / (C::BW / 16), kin = ks % (C::BW / 16);
+          seq_mma_ss<C::DESC_HI>(t, x + ((bx * C::ABOXB + kin * 32) >> 4), y + ((bx * C::YBOXB + kin * 32) >> 4), idT,
+                                 ks != 0 ? 1u : 0u);
+        }
+        if (w) umma_commit(&t_full[gb & 1u]);
       }
       __syncwarp();
-      if (++ts == C::STAGES) {
+      if (w && ++ts == C::STAGES) {
         ts = 0;
         tph ^= 1u;
       }
       return true;
     };
     auto issue_acc = [&](uint32_t gb, bool first) -> bool {
-      if (!mbar_wait(&p_full[gb % C::TB], (gb / C::TB) & 1u, status)) return false;
+      if (!mbar_wait(&p_full[gb & 1u], (gb >> 1) & 1u, status)) return false;
       if (elect_one()) {
         tc_fence_after();
         const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * as * C::YBYTES), C::YBOXB);  // MN-major
-        const uint32_t t1 = tmem + (gb % C::TB) * 128;
+        const uint32_t p = tmem + C::t1(gb), ds = tmem + C::t2(gb);
         // columns 16 ks .. + 15 of P (dS): 8 TMEM columns, those of the second 32 behind T's 32nd
 #pragma unroll
         for (int ks = 0; ks < C::YB / 16; ++ks) {
           const uint32_t at = (ks / 2) * 32 + (ks % 2) * 8, yk = y + ((ks * 16 * C::SWB) >> 4);
           if constexpr (DKV)  // dV += P^T dO
-            seq_mma_ts<C::DESC_HI>(tmem + C::ACOL + D, t1 + at, yk + (C::YBYTES >> 4), idA, (!first || ks) ? 1u : 0u);
-          seq_mma_ts<C::DESC_HI>(tmem + C::ACOL, t1 + 64 + at, yk, idA, (!first || ks) ? 1u : 0u);  // dQ, dK
+            seq_mma_ts<C::DESC_HI>(tmem + C::ACOL + D, p + at, yk + (C::YBYTES >> 4), idA, (!first || ks) ? 1u : 0u);
+          seq_mma_ts<C::DESC_HI>(tmem + C::ACOL, ds + at, yk, idA, (!first || ks) ? 1u : 0u);  // dQ, dK
         }
         umma_commit(&y_empty[as]);
       }
@@ -300,19 +306,21 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       const int j1 = real_end(u);
       if (u.j0 < j1) {
         ok = mbar_wait(&a_full[sb], aph, status);
-        auto t_next = [&](int j, uint32_t gb) {
-          if (!issue_t(j, gb)) return false;
-          if (j + 1 == j1 && elect_one()) umma_commit(&a_empty[sb]);
+        auto t_next = [&](int w, int j, uint32_t gb) {
+          if (!issue_t(w, j, gb)) return false;
+          if (w && j + 1 == j1 && elect_one()) umma_commit(&a_empty[sb]);
           __syncwarp();
           return true;
         };
-        if (ok) ok = t_next(u.j0, g);
+        if (ok) ok = t_next(0, u.j0, g);
+        if (ok) ok = t_next(1, u.j0, g);
         for (int j = u.j0; ok && j < j1; ++j) {
-          if (C::TB == 2 && j + 1 < j1) ok = t_next(j + 1, g + 1u);
+          if (j + 1 < j1) ok = t_next(0, j + 1, g + 1u);
+          if (C::SLOTS == 4 && ok && j + 1 < j1) ok = t_next(1, j + 1, g + 1u);
           if (ok && j == u.j0 && uc > 0) ok = mbar_wait(acc_empty, (uc - 1u) & 1u, status);
           if (ok) ok = issue_acc(g, j == u.j0);
+          if (C::SLOTS == 3 && ok && j + 1 < j1) ok = t_next(1, j + 1, g + 1u);
           ++g;
-          if (C::TB == 1 && ok && j + 1 < j1) ok = t_next(j + 1, g);
         }
         if (ok && elect_one()) umma_commit(acc_full);
         __syncwarp();
@@ -361,29 +369,39 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         float lse2 = 0.f, dl = 0.f;
         const bool one = !DKV && u.nb == 1;  // every key in one block
         if constexpr (!DKV) {
-          float x = 0.f;
-          if (row_on) {
-            lse2 = __ldg(lse + orow) * 1.4426950408889634f;
-            if (!one) {
-              const uint4* po = reinterpret_cast<const uint4*>(O + orow * D + half * (D / 2));
-              const uint4* pg = reinterpret_cast<const uint4*>(dO + orow * D + half * (D / 2));
+          if (row_on) lse2 = __ldg(lse + orow) * 1.4426950408889634f;
+          if (!one) {
+            // four lanes to a row, 16 rows to each warp of the pair: 64 bytes of 8 rows per load
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint4 y = __ldg(po + i), z = __ldg(pg + i);
+            for (int it = 0; it < 2; ++it) {
+              const int rr = q * 32 + half * 16 + it * 8 + (lane >> 2), r2 = u.t * a.tile + rr;
+              const bool on = rr < a.tile && r2 < u.rows;
+              const int64_t at = on ? (u.q_begin + r2 / group) * a.q_heads + u.h * group + r2 % group : 0;
+              float x = 0.f;
+              if (on) {
+                const uint4* po = reinterpret_cast<const uint4*>(O + at * D) + (lane & 3);
+                const uint4* pg = reinterpret_cast<const uint4*>(dO + at * D) + (lane & 3);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t yy = reinterpret_cast<const uint32_t*>(&y)[k], zz = reinterpret_cast<const uint32_t*>(&z)[k];
-                  x = fmaf(Half16<T>::lo(yy), Half16<T>::lo(zz), x);
-                  x = fmaf(Half16<T>::hi(yy), Half16<T>::hi(zz), x);
+                for (int i = 0; i < D / 32; ++i) {
+                  const uint4 y = __ldg(po + 4 * i), z = __ldg(pg + 4 * i);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t yy = reinterpret_cast<const uint32_t*>(&y)[k],
+                                   zz = reinterpret_cast<const uint32_t*>(&z)[k];
+                    x = fmaf(Half16<T>::lo(yy), Half16<T>::lo(zz), x);
+                    x = fmaf(Half16<T>::hi(yy), Half16<T>::hi(zz), x);
+                  }
                 }
               }
+              x += __shfl_xor_sync(0xffffffffu, x, 1);
+              x += __shfl_xor_sync(0xffffffffu, x, 2);
+              if ((lane & 3) == 0) {
+                red[rr] = x;
+                if (on) delta[at] = x;
+              }
             }
-          }
-          if (!one) {
-            red[half * 128 + row] = x;
             named_bar(bar_id, 64);
-            dl = x + red[(half ^ 1) * 128 + row];
-            if (row_on && half == 0) delta[orow] = dl;
+            dl = red[row];
           }
         }
         // DKV: lse and delta of block j's columns, one per lane
@@ -400,7 +418,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         float cl = 0.f, cd = 0.f;
         if constexpr (DKV) fetch(u.j0, cl, cd);
         for (int j = u.j0; j < j1; ++j, ++g) {
-          const uint32_t buf = g % C::TB;
+          const uint32_t buf = g & 1u;
           float* cj = cols + (j & 1) * 64;
           if constexpr (DKV) {
             cj[lane] = cl;
@@ -408,13 +426,13 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
             __syncwarp();
             if (j + 1 < j1) fetch(j + 1, cl, cd);
           }
-          if (ok) ok = mbar_wait(&t_full[buf], (g / C::TB) & 1u, status);
+          if (ok) ok = mbar_wait(&t_full[buf], (g >> 1) & 1u, status);
           tc_fence_after();
-          const uint32_t ta = tmem + lane_base + buf * 128 + half * 32;
+          const uint32_t ta = tmem + lane_base + C::t1(g) + half * 32, tb = tmem + lane_base + C::t2(g) + half * 32;
           uint32_t t1[32], t2[32];
           if (warp_on) {
             tmem_ld32(ta, t1);
-            tmem_ld32(ta + 64, t2);
+            tmem_ld32(tb, t2);
             tmem_ld_wait();
           }
           uint32_t pp[16], ds[16];
@@ -464,7 +482,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
           // over the columns of T1 and T2 that this thread read
           if (warp_on) {
             if constexpr (DKV) whale_tmem_st_cols<16>(ta, pp);
-            whale_tmem_st_cols<16>(ta + 64, ds);
+            whale_tmem_st_cols<16>(tb, ds);
           }
           whale_tmem_st_wait();
           tc_fence_before();

@@ -27,10 +27,13 @@ namespace wk {
 
 constexpr int SEQ_ROWS_WARPS = 4;
 constexpr int SEQ_ROWS_THREADS = 32 * SEQ_ROWS_WARPS;
-// Blocks per SM, and so the registers of a thread: with 16 rows of a wide head the accumulators and
-// the rows in flight need more than the 168 that three blocks leave (measured: 250 to 620 bytes
-// spilled), elsewhere three keep more loads in flight.
-constexpr int seq_rows_occupancy(int d, int nq) { return nq == 2 && d >= 128 ? 2 : 3; }
+// Blocks per SM, and so the registers of a thread. More warps hide more of a step's dependent
+// instructions, down to where registers spill: one new token over 64 8-bit caches of up to 15,000
+// keys, d = 128, takes 72 us with two blocks, 69 with three, 66 with four (and 16 keys a step, so
+// that four fit); 16 rows of a wide head need the registers of two.
+constexpr int seq_rows_occupancy(int d, int nq, bool q8) {
+  return nq == 2 ? (d >= 128 ? 2 : 3) : (d <= 64 || (d == 128 && q8) ? 4 : 3);
+}
 
 // 16-byte, 8-byte or 4-byte load of data that is read once.
 template <int BYTES>
@@ -90,7 +93,7 @@ struct SrCfg {
   static constexpr int D = D_, SRC = SRC_;
   static constexpr bool Q8 = SRC == SEQ_PAGED8;
   static constexpr int ES = Q8 ? 1 : 2;                            // bytes per element held
-  static constexpr int KS = Q8 && D <= 128 ? 32 : 16;              // keys per step of a warp
+  static constexpr int KS = 16;                                    // keys per step of a warp
   static constexpr int KB = 128;                                   // keys per block step: the unit of sharing out
   static constexpr int SUB = KB / (SEQ_ROWS_WARPS * KS);           // steps of a warp in a block step
   static constexpr int KCB = Q8 ? (D % 64 == 0 ? 16 : 8) : 16;     // bytes per load of a K row
@@ -116,7 +119,7 @@ struct SrCfg {
 
 // NQ: blocks of 8 packed rows (1 or 2).
 template <int D, typename T, int SRC, int NQ>
-__global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ))
+__global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SRC == SEQ_PAGED8))
     seq_rows_kernel(const T* __restrict__ Q, const void* __restrict__ K, const void* __restrict__ V, T* __restrict__ O,
                     float* __restrict__ lse, float* __restrict__ ws, SeqArgs a, int64_t pieces) {
   using C = SrCfg<D, SRC>;

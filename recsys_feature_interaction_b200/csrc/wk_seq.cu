@@ -136,7 +136,7 @@ constexpr int kRowsMost = 16, kRowsKB = 128;
 
 int64_t packed_rows(const SeqArgs& a) { return static_cast<int64_t>(a.max_q) * (a.q_heads / a.kv_heads); }
 int rows_nq(const SeqArgs& a) { return packed_rows(a) <= 8 ? 1 : 2; }
-int rows_pieces(int d, int nq) { return kSMs * seq_rows_occupancy(d, nq); }
+int rows_pieces(int d, int nq, bool q8) { return kSMs * seq_rows_occupancy(d, nq, q8); }
 
 // Bytes of the notes and slots of `pieces` pieces of units of r rows.
 int64_t slot_bytes(int r, int d, int64_t pieces) {
@@ -145,15 +145,15 @@ int64_t slot_bytes(int r, int d, int64_t pieces) {
 
 bool rows_cut(const SeqArgs& a) { return a.max_kv > kUncut * kRowsKB; }
 // Bytes of partial results.
-int64_t rows_ws(const SeqArgs& a, int d) {
+int64_t rows_ws(const SeqArgs& a, int d, bool q8) {
   const int nq = rows_nq(a);
-  return rows_cut(a) ? slot_bytes(8 * nq, d, rows_pieces(d, nq)) : 0;
+  return rows_cut(a) ? slot_bytes(8 * nq, d, rows_pieces(d, nq, q8)) : 0;
 }
 
 template <int D, typename T, int SRC, int NQ>
 wk_status run_rows(const void* Q, const void* K, const void* V, void* O, float* lse, float* ws, SeqArgs a,
                    cudaStream_t st) {
-  const int32_t pieces = rows_pieces(D, NQ);
+  const int32_t pieces = rows_pieces(D, NQ, SRC == SEQ_PAGED8);
   a.uncut = !rows_cut(a);
   const wk_status s = launch(seq_rows_kernel<D, T, SRC, NQ>, pieces, SEQ_ROWS_THREADS, 0, st, static_cast<const T*>(Q), K,
                              V, static_cast<T*>(O), lse, a.uncut ? nullptr : ws, a, pieces);
@@ -221,7 +221,9 @@ wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* 
                 a.q_heads, int32_t{kSMs});
 }
 
-int64_t forward_ws(const SeqArgs& a, int d) { return packed_rows(a) <= kRowsMost ? rows_ws(a, d) : tile_ws(a, d); }
+int64_t forward_ws(const SeqArgs& a, int d, bool q8) {
+  return packed_rows(a) <= kRowsMost ? rows_ws(a, d, q8) : tile_ws(a, d);
+}
 
 // Calls f with the head width and the 16-bit type as compile-time values.
 template <typename F>
@@ -376,7 +378,7 @@ wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* 
   if (!bytes) return WK_ERR_INVALID_ARG;
   const wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
-  const int64_t forward = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
+  const int64_t forward = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d, false);
   *bytes = backward ? std::max(forward, backward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d)) : forward;
   return WK_OK;
 }
@@ -515,7 +517,7 @@ wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xattn_con
   if (s != WK_OK) return s;
   if (cfg->kv_heads != cache->kv_heads || cfg->d != cache->d) return WK_ERR_INVALID_ARG;
   if (cache->dtype != WK_E4M3 && cache->dtype != cfg->dtype) return WK_ERR_UNSUPPORTED;
-  *bytes = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d);
+  *bytes = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d, cache->dtype == WK_E4M3);
   return WK_OK;
 }
 
