@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     fence_mbar_init();
   }
   // nothing of the kernels before is read above, and no TMEM is taken that they may still need
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(CR * NACC * D / 8)
   using S = SeqSlots<128, NACC * D>;
   const int32_t c = blockIdx.x / (128 / CR);
   const int r = (blockIdx.x % (128 / CR)) * CR + threadIdx.x % CR, d = (threadIdx.x / CR) * 8;
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   const SeqNote n = *S::note(ws, c);
   if (r >= n.rows) return;
   float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(CR * NACC * D / 8)
 // Zeros in the rows between a sequence's last key and the next sequence (padded batches).
 template <typename T>
 __global__ void seq_zero_padding_kernel(T* __restrict__ dK, T* __restrict__ dV, int64_t row_elems, SeqArgs a) {
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   const SeqSpan kv = seq_keys<SEQ_JAGGED>(a, blockIdx.x);
   const int64_t at = (kv.begin + kv.len) * row_elems / 8;
   const int64_t n = static_cast<int64_t>(kv.room - kv.len) * row_elems / 8;

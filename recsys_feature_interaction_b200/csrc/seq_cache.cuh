@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(SEQ_COPY_THREADS)
                        uint8_t* __restrict__ eK, uint8_t* __restrict__ eV, SeqArgs a, int32_t chunks) {
   constexpr int CH = D / 32;  // chunks of 8 elements per lane
   const SeqCopyPlace p(a, chunks);
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   const SeqSpan q = seq_queries(a, p.b);
   const SeqSpan kv = seq_cached(a.kv_lens, p.b, static_cast<int64_t>(a.table_width) << a.page_shift, INT32_MAX);
   if (q.bad || kv.bad || kv.len < q.len) {
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(SEQ_COPY_THREADS)
                       SeqArgs a, int32_t chunks) {
   constexpr int CH = D / 32;
   const SeqCopyPlace p(a, chunks);
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   const SeqSpan kv = seq_keys<SRC>(a, p.b);
   const SeqSpan out = seq_span(a.kv_off, nullptr, p.b, a.total_kv, INT32_MAX);
   if ((kv.bad || out.bad || out.room < kv.len) && threadIdx.x == 0) flag_error(a.status, kFlagBadShape);

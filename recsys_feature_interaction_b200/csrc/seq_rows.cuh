@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
   __shared__ __align__(16) float sm_o[SEQ_ROWS_WARPS][R][PITCH];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const float scale_log2 = a.scale * 1.4426950408889634f;
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   const SeqPlace place = seq_place<SeqPlan<R, C::KB, SRC>, SEQ_ROWS_THREADS>(a, blockIdx.x, pieces, sh, blockIdx.x == 0);
   using S = SeqSlots<R, D>;
   bool left = false;  // a unit left unfinished

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     fence_mbar_init();
   }
   // nothing of the kernels before is read above, and no TMEM is taken that they may still need
-  cudaGridDependencySynchronize();
+  seq_wait_before();
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
