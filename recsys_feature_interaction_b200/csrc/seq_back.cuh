@@ -4,7 +4,7 @@
 //   dS = P (dP - delta) scale,   dQ = dS K,   dK = dS^T Q,   dV = P^T dO.
 // Two kernels of one shape, so that every sum has one owner and nothing is added with atomics (the
 // results do not depend on the order in which blocks run):
-//   DQ    128 packed query rows stand (Q, dO), 64-key blocks go by (K, V):
+//   DQ    128 packed query rows stand (Q, dO), blocks of 128 or 64 keys go by (K, V):
 //         T1 = Q K^T, T2 = dO V^T, dQ += dS K
 //   DKV   128 keys stand (K, V), blocks of up to 64 packed query rows go by (Q, dO), so that a key
 //         head's sum over its query heads is part of the product:
@@ -15,7 +15,7 @@
 // Both operands of T1, T2 come from shared memory, the tiles that go by are read a second time as
 // MN-major operands of the accumulating products, whose A operands (P, dS) are written over the
 // columns of T1, T2 that the same thread has just read, so the element-wise warps (two per lane
-// quarter, 32 columns each) need no barrier among themselves. T1 and T2 of the next block are
+// quarter, half the columns each) need no barrier among themselves. T1 and T2 of the next block are
 // computed under this one's element-wise work as far as TMEM has room beside the accumulators.
 //
 // delta comes from the stored (rounded) O, except where one block holds all keys of a row: there it
@@ -35,7 +35,10 @@ template <int D_, bool DKV_>
 struct SbCfg {
   static constexpr int D = D_;
   static constexpr bool DKV = DKV_;
-  static constexpr int R = 128, YB = 64;
+  // Rows that go by at a time. An MMA of N = 64 with both operands in shared memory reads 6 KB in its 32
+  // cycles, one of N = 128 8 KB in 64: 128 where TMEM holds three results of that width (not beside
+  // two accumulators, nor beside one of 160).
+  static constexpr int R = 128, YB = !DKV && D <= 128 ? 128 : 64;
   static constexpr int BW = (D % 64 == 0) ? 64 : 32;
   static constexpr int SWB = BW * 2;
   static constexpr uint32_t SWMODE = BW == 64 ? 2u : 4u;
@@ -58,13 +61,13 @@ struct SbCfg {
   static constexpr int STAGES = STAGES_RAW > 4 ? 4 : STAGES_RAW;
   static constexpr int RAW = FIXED + 2 * SBUF * AB + STAGES * 2 * YBYTES;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;  // one block per SM: its TMEM is its own
-  // TMEM: SLOTS places of 64 columns that T1 and T2 of the blocks take in turn, then the accumulators.
+  // TMEM: SLOTS places of YB columns that T1 and T2 of the blocks take in turn, then the accumulators.
   // With four, both of the next block are computed under this one's element-wise work; with three
-  // (dK and dV of d = 160) its T1 is.
-  static constexpr int SLOTS = 256 + NACC * D <= 512 ? 4 : 3;
-  static constexpr int ACOL = SLOTS * 64;
-  static __device__ __forceinline__ uint32_t t1(uint32_t g) { return (2u * g) % SLOTS * 64u; }
-  static __device__ __forceinline__ uint32_t t2(uint32_t g) { return (2u * g + 1u) % SLOTS * 64u; }
+  // its T1 is.
+  static constexpr int SLOTS = 4 * YB + NACC * D <= 512 ? 4 : 3;
+  static constexpr int ACOL = SLOTS * YB;
+  static __device__ __forceinline__ uint32_t t1(uint32_t g) { return (2u * g) % SLOTS * YB; }
+  static __device__ __forceinline__ uint32_t t2(uint32_t g) { return (2u * g + 1u) % SLOTS * YB; }
   static constexpr int THREADS = 384;
   static_assert(ACOL + NACC * D <= 512 && STAGES >= 2 && AB % 1024 == 0 && YBYTES % 1024 == 0, "layout");
   static_assert((2 * SBUF + 2 * STAGES + 7 + 2 * NU) * 8 + 8 <= BARB, "barriers");
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       SeqUnit u;
-      const int per_tile = DKV ? 128 : a.tile / group, per_block = DKV ? a.block / group : 64;  // tokens
+      const int per_tile = DKV ? 128 : a.tile / group, per_block = DKV ? a.block / group : a.block;  // tokens
       while (ok && unit_take(u)) {
         const int j1 = real_end(u);
         if (u.j0 < j1) {
@@ -288,7 +291,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         tc_fence_after();
         const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * as * C::YBYTES), C::YBOXB);  // MN-major
         const uint32_t p = tmem + C::t1(gb), ds = tmem + C::t2(gb);
-        // columns 16 ks .. + 15 of P (dS): 8 TMEM columns, those of the second 32 behind T's 32nd
+        // columns 16 ks .. + 15 of P (dS): 8 TMEM columns, each 32 behind the first of T's own 32
 #pragma unroll
         for (int ks = 0; ks < C::YB / 16; ++ks) {
           const uint32_t at = (ks / 2) * 32 + (ks % 2) * 8, yk = y + ((ks * 16 * C::SWB) >> 4);
@@ -428,15 +431,19 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
           }
           if (ok) ok = mbar_wait(&t_full[buf], (g >> 1) & 1u, status);
           tc_fence_after();
-          const uint32_t ta = tmem + lane_base + C::t1(g) + half * 32, tb = tmem + lane_base + C::t2(g) + half * 32;
+          const uint32_t ta = tmem + lane_base + C::t1(g) + half * (C::YB / 2);
+          const uint32_t tb = tmem + lane_base + C::t2(g) + half * (C::YB / 2);
           uint32_t t1[32], t2[32];
-          if (warp_on) {
-            tmem_ld32(ta, t1);
-            tmem_ld32(tb, t2);
-            tmem_ld_wait();
-          }
-          uint32_t pp[16], ds[16];
+          auto load = [&](int at) {
+            if (warp_on) {
+              tmem_ld32(ta + at, t1);
+              tmem_ld32(tb + at, t2);
+              tmem_ld_wait();
+            }
+          };
           if constexpr (DKV) {
+            load(0);
+            uint32_t pp[16], ds[16];
 #pragma unroll
             for (int c4 = 0; c4 < 8; ++c4) {
               const float4 l4 = *reinterpret_cast<const float4*>(cj + 4 * c4);
@@ -453,36 +460,50 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
               ds[2 * c4] = Half16<T>::pack2(s[0], s[1]);
               ds[2 * c4 + 1] = Half16<T>::pack2(s[2], s[3]);
             }
+            if (warp_on) {  // over the columns of T1 and T2 that this thread read
+              whale_tmem_st_cols<16>(ta, pp);
+              whale_tmem_st_cols<16>(tb, ds);
+            }
           } else {
-            const int valid = u.len - j * a.block - half * 32;
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              t1[c] = __float_as_uint(whale_ex2(fmaf(__uint_as_float(t1[c]), scale_log2, -lse2)));
-            if (valid < 32) {
+            // P over t1; keys behind the sequence's end count for nothing
+            auto weights = [&](int at) {
+              const int valid = u.len - j * a.block - half * (C::YB / 2) - at;
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (c >= valid) t1[c] = t2[c] = 0u;
-            }
+                t1[c] = __float_as_uint(whale_ex2(fmaf(__uint_as_float(t1[c]), scale_log2, -lse2)));
+              if (valid < 32) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (c >= valid) t1[c] = t2[c] = 0u;
+              }
+            };
             if (one) {
               float x = 0.f;
+#pragma unroll 1
+              for (int at = 0; at < C::YB / 2; at += 32) {
+                load(at);
+                weights(at);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) x = fmaf(__uint_as_float(t1[c]), __uint_as_float(t2[c]), x);
+                for (int c = 0; c < 32; ++c) x = fmaf(__uint_as_float(t1[c]), __uint_as_float(t2[c]), x);
+              }
               red[half * 128 + row] = x;
               named_bar(bar_id, 64);
               dl = x + red[(half ^ 1) * 128 + row];
               if (row_on && half == 0) delta[orow] = dl;
             }
+#pragma unroll 1
+            for (int at = 0; at < C::YB / 2; at += 32) {
+              load(at);
+              weights(at);
+              uint32_t ds[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float s0 = __uint_as_float(t1[2 * c]) * ((__uint_as_float(t2[2 * c]) - dl) * a.scale);
-              const float s1 = __uint_as_float(t1[2 * c + 1]) * ((__uint_as_float(t2[2 * c + 1]) - dl) * a.scale);
-              ds[c] = Half16<T>::pack2(s0, s1);
+              for (int c = 0; c < 16; ++c) {
+                const float s0 = __uint_as_float(t1[2 * c]) * ((__uint_as_float(t2[2 * c]) - dl) * a.scale);
+                const float s1 = __uint_as_float(t1[2 * c + 1]) * ((__uint_as_float(t2[2 * c + 1]) - dl) * a.scale);
+                ds[c] = Half16<T>::pack2(s0, s1);
+              }
+              if (warp_on) whale_tmem_st_cols<16>(tb + at, ds);
             }
-          }
-          // over the columns of T1 and T2 that this thread read
-          if (warp_on) {
-            if constexpr (DKV) whale_tmem_st_cols<16>(ta, pp);
-            whale_tmem_st_cols<16>(tb, ds);
           }
           whale_tmem_st_wait();
           tc_fence_before();

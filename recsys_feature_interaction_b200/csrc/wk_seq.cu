@@ -286,7 +286,7 @@ struct RunBackward {
     SeqArgs x = a;
     const int group = a.q_heads / a.kv_heads;
     x.tile = DKV ? 128 : group * (128 / group);
-    x.block = DKV ? dkv_block(a) : 64;
+    x.block = DKV ? dkv_block(a) : C::YB;
     x.uncut = !(DKV ? dkv_cut(a) : dq_cut(a));
     auto fn = seq_back_kernel<D, T, DKV>;
     wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
@@ -302,7 +302,7 @@ struct RunBackward {
 
   template <int D, typename T>
   wk_status operator()() const {
-    constexpr int BW = SbCfg<D, false>::BW;
+    constexpr int BW = SbCfg<D, false>::BW, YB = SbCfg<D, false>::YB;
     const int group = a.q_heads / a.kv_heads;
     // without rows (or without keys) the tensors may be NULL; their maps are then not used
     const void* any = a.total_q > 0 ? Q : K;
@@ -314,8 +314,8 @@ struct RunBackward {
       return map_tokens<T>(dv, m, p, any, D, a.kv_heads, a.total_kv, stride, BW, 1, n);
     };
     CUtensorMap q[4], k[4];  // the maps of DQ and of DKV
-    if (!rows(&q[0], Q, a.q_stride, 128) || !rows(&q[1], dO, od, 128) || !keys(&q[2], K, a.k_stride, 64) ||
-        !keys(&q[3], V, a.v_stride, 64) || !keys(&k[0], K, a.k_stride, 128) || !keys(&k[1], V, a.v_stride, 128) ||
+    if (!rows(&q[0], Q, a.q_stride, 128) || !rows(&q[1], dO, od, 128) || !keys(&q[2], K, a.k_stride, YB) ||
+        !keys(&q[3], V, a.v_stride, YB) || !keys(&k[0], K, a.k_stride, 128) || !keys(&k[1], V, a.v_stride, 128) ||
         !rows(&k[2], Q, a.q_stride, 64) || !rows(&k[3], dO, od, 64))
       return WK_ERR_UNSUPPORTED;
     float* delta = static_cast<float*>(workspace);
