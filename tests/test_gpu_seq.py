@@ -99,6 +99,10 @@ SHAPES = [
     ([512], [700], 2, 2, 64, 3.0),
     ([2], [9000], 8, 2, 128, 1.0),
     ([1] * 5, [4097, 0, 3, 1500, 64], 10, 2, 160, 1.0),
+    ([3, 5], [700, 130], 64, 1, 32, 1.0),    # 64 query heads share a key head: two tokens to a tile
+    ([7, 2], [600, 31], 48, 1, 64, 1.0),
+    ([2, 40], [900, 129], 22, 2, 128, 1.0),  # 11 to a key head: tiles of 121 rows, blocks of 55
+    ([0, 0, 4], [10, 600, 0], 2, 2, 64, 1.0),
 ]
 
 
@@ -606,3 +610,105 @@ def test_broken_tables_are_told_and_kept_inside():
     O2, _ = j.forward()
     _ok()
     assert torch.equal(O2[:50], O[:50])
+
+
+# ---------------------------------------------------------------- sizes at the edges
+
+@pytest.mark.parametrize("rows", [1, 23])
+def test_thousands_of_short_sequences(rows):
+    """More units than blocks of the grid by far, most of them of one key block or none."""
+    r = np.random.RandomState(5)
+    n = [int(x) for x in r.randint(0, rows + 1, 3000)]
+    kv = [int(x) for x in r.randint(0, 40, 3000)]
+    n[0], kv[1] = rows, 700  # some are cut
+    j = Jagged(n, kv, 2, 2, 32, "bf16")
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    j.check(O, L, grads)
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_a_long_sequence_among_short_ones(n):
+    """One sequence is most of the work: it is cut over nearly every block."""
+    gen = torch.Generator().manual_seed(8)
+    c = Cached([70001, 5, 300], 1, 64, "bf16", 128, 8)
+    q = _rand(gen, c.dt, n + 2, 2, 64, std=0.2)
+    O, L = _attend(c, q, U.offsets([n, 1, 1]), n, True)
+    _ok()
+    _check_attend(c, q, [n, 1, 1], O, L, True)
+
+
+def test_nothing_at_all():
+    """No keys anywhere, no rows anywhere, no sequences: zeros, or nothing written."""
+    j = Jagged([5, 0], [0, 0], 2, 2, 64, "bf16", behind=0)
+    j.max_kv = 0
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    assert (O == 0).all() and torch.isneginf(L).all() and (grads[0] == 0).all()
+    j = Jagged([0, 0], [5, 300], 2, 2, 64, "bf16", behind=0)
+    j.max_q = 0
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    assert (grads[1] == 0).all() and (grads[2] == 0).all()
+    empty = torch.zeros(1, dtype=torch.int32, device="cuda")
+    j.q_off = j.kv_off = empty
+    j.n = []
+    wk.wk_xattn_forward(j.q, j.k, j.v, O, empty, empty, 0, 0, workspace=j.workspace(False))
+    _ok()
+
+
+@pytest.mark.parametrize("d", [64, 160])
+def test_infinities_in_keys_that_take_part(d):
+    """An infinite key gives NaN or the winning weight as the definition does; other sequences keep theirs."""
+    j = Jagged([40, 40], [200, 200], 1, 1, d, "bf16", behind=0)
+    clean, _ = j.forward()
+    j.k[5] = float("inf")
+    O, _ = j.forward()
+    _ok()
+    assert torch.isnan(O[:40].float()).all()
+    assert torch.equal(O[40:], clean[40:])
+
+
+def test_two_streams_at_once():
+    """Two calls on two streams, each with a workspace of its own, give what they give alone."""
+    a = Jagged([64] * 20, [2000] * 20, 4, 2, 128, "bf16", seed=1)
+    b = Jagged([3] * 50, [900] * 50, 4, 4, 64, "f16", seed=2)
+    alone = []
+    for j in (a, b):
+        O, L = j.forward()
+        alone.append([O, L, *j.backward(O, L)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    keep = [(j.workspace(False), j.workspace(True)) for j in (a, b)]
+    outs = []
+    torch.cuda.synchronize()
+    for j, s, (w0, w1) in zip((a, b), streams, keep):
+        with torch.cuda.stream(s):
+            O, L = torch.empty_like(j.q), torch.empty(j.q.shape[:2], device="cuda")
+            grads = [torch.empty_like(t) for t in (j.q, j.k, j.v)]
+            for _ in range(3):
+                wk.wk_xattn_forward(j.q, j.k, j.v, O, j.q_off, j.kv_off, j.max_q, j.max_kv, lse=L, workspace=w0)
+                wk.wk_xattn_backward(j.q, j.k, j.v, O, L, j.g, *grads, j.q_off, j.kv_off, j.max_q, j.max_kv,
+                                     workspace=w1)
+            outs.append([O, L, *grads])
+    _ok()
+    for j, x, y in zip((a, b), outs, alone):
+        ends = [sum(j.n)] * 3 + [sum(j.kv)] * 2
+        for t, u, m in zip(x, y, ends):
+            assert torch.equal(t[:m], u[:m])
+
+
+def test_a_stream_that_is_not_the_current_one():
+    j = Jagged([33, 2], [500, 700], 2, 1, 64, "f16", behind=0)
+    want, _ = j.forward()
+    _ok()
+    s = torch.cuda.Stream()
+    O = torch.zeros_like(want)
+    ws = j.workspace(False)
+    torch.cuda.synchronize()
+    wk.wk_xattn_forward(j.q, j.k, j.v, O, j.q_off, j.kv_off, j.max_q, j.max_kv, workspace=ws, stream=s)
+    s.synchronize()
+    assert torch.equal(O, want)
