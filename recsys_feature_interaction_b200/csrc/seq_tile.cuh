@@ -597,10 +597,12 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
                 if (at + c >= kvalid) sr[c] = 0xFF800000u;  // -inf
             }
           };
-          load_half(KB / 2);
-          float mh = seq_max<KB / 2>(sr);
-          load_half(0);
-          mh = seq_max2(mh, seq_max<KB / 2>(sr));
+          float mh = -INFINITY;
+#pragma unroll 1
+          for (int at = KB / 2; at >= 0; at -= KB / 2) {
+            load_half(at);
+            mh = seq_max2(mh, seq_max<KB / 2>(sr));
+          }
           float mprev = -INFINITY;
           if (j > u.j0) {
             named_bar(hear_id, 64);
