@@ -639,6 +639,8 @@ def _tokens(t, name):
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError("the heads of a token of %s must be dense" % name)
+    if s0 < h * d and n > 1:  # an expanded tensor: the library reads 0 as "dense"
+        raise ValueError("the tokens of %s overlap" % name)
     return n, h, d, (s0 if n > 1 else h * d)
 
 

@@ -52,6 +52,23 @@ __device__ __forceinline__ SeqSpan seq_queries(const SeqArgs& a, int64_t b) {
 // end was slower: a training step at the 2-layer shape took 145 us, so 133.)
 __device__ __forceinline__ void seq_wait_before() { cudaGridDependencySynchronize(); }
 
+// mbar_wait that gives up early only for a wait that ran out: sequences that are in order keep their
+// results in a call (or after one) whose tables set another flag.
+__device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, unsigned* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long start = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0u) {
+      if (*reinterpret_cast<const volatile unsigned*>(status) & kFlagTimeout) return false;
+      if (clock64() - start > WK_WAIT_LIMIT) {
+        flag_error(status, kFlagTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // 2^(e - 127) of a cache row's exponent byte; NaN for 255.
 __device__ __forceinline__ float seq_pow(uint32_t e) {
   return __uint_as_float(e == 255 ? 0x7FC00000u : (e == 0 ? 0x00400000u : e << 23));

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
   uint32_t ui = 0;
   auto unit_take = [&](SeqUnit& u) -> bool {
     const uint32_t s = ui % C::NU;
-    if (!mbar_wait(&u_full[s], (ui / C::NU) & 1u, status)) return false;
+    if (!seq_wait(&u_full[s], (ui / C::NU) & 1u, status)) return false;
     u = unit[s];
     return u.b >= 0;
   };
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       for (;;) {
         const bool more = w.next(a);
         const uint32_t s = ui % C::NU;
-        if (!mbar_wait(&u_empty[s], ((ui / C::NU) & 1u) ^ 1u, status)) break;
+        if (!seq_wait(&u_empty[s], ((ui / C::NU) & 1u) ^ 1u, status)) break;
         if (!more) w.u.b = -1;
         unit[s] = w.u;
         mbar_arrive(&u_full[s]);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       while (ok && unit_take(u)) {
         const int j1 = real_end(u);
         if (u.j0 < j1) {
-          ok = mbar_wait(&a_empty[sb], aph ^ 1u, status);
+          ok = seq_wait(&a_empty[sb], aph ^ 1u, status);
           if (ok) {
             mbar_arrive_expect_tx(&a_full[sb], static_cast<uint32_t>(2 * a.tile * D * 2));
             const int h = DKV ? u.h : u.h * group;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
             }
           }
           for (int j = u.j0; ok && j < j1; ++j) {
-            ok = mbar_wait(&y_empty[s], ph ^ 1u, status);
+            ok = seq_wait(&y_empty[s], ph ^ 1u, status);
             if (!ok) break;
             mbar_arrive_expect_tx(&y_full[s], static_cast<uint32_t>(2 * a.block * D * 2));
             const int h = DKV ? u.h * group : u.h;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     // the block in ring place ts: T1 (w = 0, the first to need it) and T2 (w = 1, the last)
     auto issue_t = [&](int w, int j, uint32_t gb) -> bool {
       if (w == 0) {
-        if (!mbar_wait(&y_full[ts], tph, status)) return false;
+        if (!seq_wait(&y_full[ts], tph, status)) return false;
         const int valid = min(a.block, passing(u) - j * a.block);
         if (valid < C::YB) {
           constexpr int UR = C::SWB / 16;  // 16-byte units of a box row
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
       return true;
     };
     auto issue_acc = [&](uint32_t gb, bool first) -> bool {
-      if (!mbar_wait(&p_full[gb & 1u], (gb >> 1) & 1u, status)) return false;
+      if (!seq_wait(&p_full[gb & 1u], (gb >> 1) & 1u, status)) return false;
       if (elect_one()) {
         tc_fence_after();
         const uint32_t y = seq_desc_lo(smem_u32(sY + 2 * as * C::YBYTES), C::YBOXB);  // MN-major
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     while (ok && unit_take(u)) {
       const int j1 = real_end(u);
       if (u.j0 < j1) {
-        ok = mbar_wait(&a_full[sb], aph, status);
+        ok = seq_wait(&a_full[sb], aph, status);
         auto t_next = [&](int w, int j, uint32_t gb) {
           if (!issue_t(w, j, gb)) return false;
           if (w && j + 1 == j1 && elect_one()) umma_commit(&a_empty[sb]);
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         for (int j = u.j0; ok && j < j1; ++j) {
           if (j + 1 < j1) ok = t_next(0, j + 1, g + 1u);
           if (C::SLOTS == 4 && ok && j + 1 < j1) ok = t_next(1, j + 1, g + 1u);
-          if (ok && j == u.j0 && uc > 0) ok = mbar_wait(acc_empty, (uc - 1u) & 1u, status);
+          if (ok && j == u.j0 && uc > 0) ok = seq_wait(acc_empty, (uc - 1u) & 1u, status);
           if (ok) ok = issue_acc(g, j == u.j0);
           if (C::SLOTS == 3 && ok && j + 1 < j1) ok = t_next(1, j + 1, g + 1u);
           ++g;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
             __syncwarp();
             if (j + 1 < j1) fetch(j + 1, cl, cd);
           }
-          if (ok) ok = mbar_wait(&t_full[buf], (g >> 1) & 1u, status);
+          if (ok) ok = seq_wait(&t_full[buf], (g >> 1) & 1u, status);
           tc_fence_after();
           const uint32_t ta = tmem + lane_base + C::t1(g) + half * (C::YB / 2);
           const uint32_t tb = tmem + lane_base + C::t2(g) + half * (C::YB / 2);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[buf]);
         }
-        if (ok) ok = mbar_wait(acc_full, uc & 1u, status);
+        if (ok) ok = seq_wait(acc_full, uc & 1u, status);
         tc_fence_after();
         ++uc;
         if (warp_on) {

@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   uint32_t ui = 0;
   auto unit_take = [&](SeqUnit& u) -> bool {
     const uint32_t s = ui % C::NU;
-    if (!mbar_wait(&u_full[s], (ui / C::NU) & 1u, status)) return false;
+    if (!seq_wait(&u_full[s], (ui / C::NU) & 1u, status)) return false;
     u = unit[s];
     return u.b >= 0;
   };
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       for (;;) {
         const bool more = w.next(a);
         const uint32_t s = ui % C::NU;
-        if (!mbar_wait(&u_empty[s], ((ui / C::NU) & 1u) ^ 1u, status)) break;
+        if (!seq_wait(&u_empty[s], ((ui / C::NU) & 1u) ^ 1u, status)) break;
         if (!more) w.u.b = -1;
         unit[s] = w.u;
         mbar_arrive(&u_full[s]);
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     SeqUnit u;
     const int tokens = a.tile / group;  // per Q tile: its rows are (token, head) with the head first
     auto load_q = [&]() -> bool {
-      if (!mbar_wait(q_empty, qph ^ 1u, status)) return false;
+      if (!seq_wait(q_empty, qph ^ 1u, status)) return false;
       if (elect_one()) {
         mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(a.tile * D * 2));
 #pragma unroll
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           }
         }
       }
-      if (!mbar_wait(&kv_empty[s], ph ^ 1u, status)) return false;
+      if (!seq_wait(&kv_empty[s], ph ^ 1u, status)) return false;
       uint8_t* dst = tiles + s * C::TILEB;
       if constexpr (SRC == SEQ_JAGGED) {
         if (elect_one()) {
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       }
     };
     auto issue_s = [&](uint32_t gb, bool last) -> bool {
-      if (!mbar_wait(&kv_full[s], ph, status)) return false;
+      if (!seq_wait(&kv_full[s], ph, status)) return false;
       if (elect_one()) {
         tc_fence_after();
         const uint32_t k = seq_desc_lo(smem_u32(tiles + s * C::TILEB), 16);
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       return true;
     };
     auto issue_pv = [&](int j, bool last, uint32_t gj, bool first) -> bool {
-      if (!mbar_wait(&kv_full[s], ph, status)) return false;
+      if (!seq_wait(&kv_full[s], ph, status)) return false;
       // MN-major V: BW-column atoms BOXB apart, 8-key groups 8 * SWB apart
       const uint32_t v = seq_desc_lo(smem_u32(tiles + s * C::TILEB), C::BOXB);
       const int valid = u.len - j * KB;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const uint32_t buf = gj % C::NS;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // the first half's product runs under the second's softmax
-        if (!mbar_wait(&p_full[2 * buf + half], (gj / C::NS) & 1u, status)) return false;
+        if (!seq_wait(&p_full[2 * buf + half], (gj / C::NS) & 1u, status)) return false;
         if (elect_one()) {
           tc_fence_after();
 #pragma unroll
@@ -516,12 +516,12 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     while (ok && unit_take(u)) {
       const int j1 = seq_real_end(a, u, group, a.tile, KB);
       if (u.j0 < j1) {
-        ok = mbar_wait(q_full, uc & 1u, status);
+        ok = seq_wait(q_full, uc & 1u, status);
         for (int k = 0; ok && k < min(C::AHEAD, j1 - u.j0); ++k) ok = issue_s(g + k, u.j0 + k + 1 == j1);
         for (int j = u.j0; ok && j < j1; ++j) {
           if (j + C::AHEAD < j1) ok = issue_s(g + C::AHEAD, j + C::AHEAD + 1 == j1);
           // O is free once the softmax warps have read the unit before
-          if (ok && j == u.j0 && uc > 0) ok = mbar_wait(o_empty, (uc - 1u) & 1u, status);
+          if (ok && j == u.j0 && uc > 0) ok = seq_wait(o_empty, (uc - 1u) & 1u, status);
           if (ok) ok = issue_pv(j, j + 1 == j1, g, j == u.j0);
           ++g;
         }
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         for (int j = u.j0; j < j1; ++j, ++g) {
           if ((g & 1u) != static_cast<uint32_t>(grp)) continue;
           const uint32_t buf = g % C::NS;
-          if (ok) ok = mbar_wait(&s_full[buf], (g / C::NS) & 1u, status);
+          if (ok) ok = seq_wait(&s_full[buf], (g / C::NS) & 1u, status);
           tc_fence_after();
           float scale_log2 = a.scale * 1.4426950408889634f;
           if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           if (j > u.j0 && __any_sync(0xffffffffu, need)) {
             // the maximum was raised: O must hold every earlier block before it is rescaled
             const uint32_t gp = g - 1u;
-            if (ok) ok = mbar_wait(&p_empty[gp % C::NS], (gp / C::NS) & 1u, status);
+            if (ok) ok = seq_wait(&p_empty[gp % C::NS], (gp / C::NS) & 1u, status);
             tc_fence_after();
             const float factor = need ? whale_ex2(mprev - mnew) : 1.f;
             if (warp_on) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) lt += lrow[x * R + row] * whale_ex2(mrow[x * R + row] - mz);
         named_bar(pair_id, 64);  // before the next unit overwrites them
-        if (ok) ok = mbar_wait(&p_empty[gl % C::NS], (gl / C::NS) & 1u, status);
+        if (ok) ok = seq_wait(&p_empty[gl % C::NS], (gl / C::NS) & 1u, status);
         tc_fence_after();
         if (warp_on) {
           float vs = 1.f;  // V's reference exponent
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             }
           }
         }
-        if (ok) ok = mbar_wait(&kv_empty[s], ph ^ 1u, status);
+        if (ok) ok = seq_wait(&kv_empty[s], ph ^ 1u, status);
         uint8_t* dst = tiles + s * C::TILEB;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {

@@ -69,6 +69,11 @@ wk_status check_cache(const wk_cache* c) {
   return WK_OK;
 }
 
+// Bytes of a cache's K (or V).
+int64_t cache_bytes(const wk_cache& c) {
+  return static_cast<int64_t>(c.num_pages) * c.kv_heads * c.page_size * c.d * (c.dtype == WK_E4M3 ? 1 : 2);
+}
+
 int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 SeqArgs make_args(const wk_xattn_config& c, const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_lens,
@@ -401,7 +406,8 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
   const int64_t ob = extent(cfg->total_q, static_cast<int64_t>(cfg->q_heads) * cfg->d, cfg->q_heads, cfg->d);
   if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)) ||
       overlap(O, ob, K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)) ||
-      overlap(O, ob, V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)))
+      overlap(O, ob, V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)) ||
+      overlap(O, ob, workspace, need) || overlap(O, ob, lse, cfg->total_q * cfg->q_heads * 4))
     return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
@@ -471,6 +477,11 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
     return WK_ERR_INVALID_ARG;
   SeqArgs a = make_args(cfg, new_off, nullptr, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
+  const int64_t cb = cache_bytes(*cache), kb = extent(total_new, a.k_stride, cfg.kv_heads, cfg.d),
+                vb = extent(total_new, a.v_stride, cfg.kv_heads, cfg.d);
+  if (overlap(cache->K, cb, cache->V, cb) || overlap(cache->K, cb, K, kb) || overlap(cache->K, cb, V, vb) ||
+      overlap(cache->V, cb, K, kb) || overlap(cache->V, cb, V, vb))
+    return WK_ERR_INVALID_ARG;
   const int32_t chunks = (max_new + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
   const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
   if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
@@ -494,7 +505,10 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
       !al4(out_off) || !al4(table) || !al4(kv_lens))
     return WK_ERR_INVALID_ARG;
   const int64_t bytes = total * cache->kv_heads * cache->d * 2;
-  if (overlap(K, bytes, V, bytes)) return WK_ERR_INVALID_ARG;
+  const int64_t cb = cache_bytes(*cache);
+  if (overlap(K, bytes, V, bytes) || overlap(K, bytes, cache->K, cb) || overlap(K, bytes, cache->V, cb) ||
+      overlap(V, bytes, cache->K, cb) || overlap(V, bytes, cache->V, cb))
+    return WK_ERR_INVALID_ARG;
   wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
   SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
@@ -537,7 +551,11 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   cache_args(&a, *cache, table, table_width);
   a.causal = causal != 0;
   const int64_t ob = cfg->total_q * cfg->q_heads * cfg->d * 2;
-  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d))) return WK_ERR_INVALID_ARG;
+  const int64_t cb = cache_bytes(*cache);
+  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)) || overlap(O, ob, workspace, need) ||
+      overlap(O, ob, lse, cfg->total_q * cfg->q_heads * 4) || overlap(O, ob, cache->K, cb) ||
+      overlap(O, ob, cache->V, cb))
+    return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
   if (s != WK_OK) return s;

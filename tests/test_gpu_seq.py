@@ -612,6 +612,24 @@ def test_broken_tables_are_told_and_kept_inside():
     assert torch.equal(O2[:50], O[:50])
 
 
+def test_a_flag_left_unread_spoils_nothing():
+    """A broken table in one sequence, its status not read: the others of that call, and a later call, are right."""
+    gen = torch.Generator().manual_seed(4)
+    c = Cached([600, 700], 2, 64, "bf16", 16, 16)
+    q = _rand(gen, c.dt, 60, 4, 64)
+    off = U.offsets([30, 30])
+    good, lse = _attend(c, q, off, 30, True)
+    _ok()
+    keep = c.table.clone()
+    c.table[0, 20] = 1 << 20
+    O, _ = _attend(c, q, off, 30, True)
+    assert torch.equal(O[30:], good[30:])
+    c.table.copy_(keep)
+    O, L = _attend(c, q, off, 30, True)
+    assert torch.equal(O, good) and torch.equal(L, lse)
+    assert _status() == wk.WK_ERR_DEVICE
+
+
 # ---------------------------------------------------------------- sizes at the edges
 
 @pytest.mark.parametrize("rows", [1, 23])

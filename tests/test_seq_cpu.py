@@ -194,6 +194,7 @@ def test_pointers_that_are_refused(L):
         assert call(**{"a%d" % i: FAKE + 2}) == wk.WK_ERR_INVALID_ARG
     assert call(a6=_far(1) + 64) == wk.WK_ERR_INVALID_ARG       # O over Q
     assert call(a6=_far(2)) == wk.WK_ERR_INVALID_ARG            # O over K
+    assert call(a7=_far(4) + 16) == wk.WK_ERR_INVALID_ARG       # lse in O
     assert call(a9=-1) == wk.WK_ERR_INVALID_ARG
     e = _cfg(batch=0)
     assert L.wk_xattn_forward(ctypes.byref(e), *([None] * 9), 0, None) == wk.WK_OK
@@ -269,6 +270,15 @@ def test_cache_calls_that_are_refused(L):
     r = [FAKE, 4, FAKE, FAKE, _far(5), _far(6), wk.WK_BF16, 2, 100, 50, None]
     assert L.wk_cache_read(ctypes.byref(q8), *(r[:5] + [_far(5) + 128] + r[6:])) == wk.WK_ERR_INVALID_ARG  # V over K
     assert L.wk_cache_read(ctypes.byref(q16), *r) == wk.WK_ERR_UNSUPPORTED
+    # buffers that lie over one another
+    assert write(_cache(V=_far(1) + 64)) == wk.WK_ERR_INVALID_ARG
+    assert write(q8, a0=_far(1)) == wk.WK_ERR_INVALID_ARG and write(q8, a1=_far(1) + 128) == wk.WK_ERR_INVALID_ARG
+    assert L.wk_cache_read(ctypes.byref(q8), *(r[:4] + [_far(2)] + r[5:])) == wk.WK_ERR_INVALID_ARG
+    cfg = _cfg()
+    att = [_far(7), FAKE, FAKE, 4, FAKE, 1, _far(8), None, _far(9), 1 << 30, None]
+    for over in (_far(7) + 32, _far(1) + 16, _far(2)):
+        assert L.wk_cache_attention(ctypes.byref(q8), ctypes.byref(cfg), *(att[:6] + [over] + att[7:])) \
+            == wk.WK_ERR_INVALID_ARG
 
 
 def test_the_binding_refuses(L):
@@ -283,7 +293,7 @@ def test_the_binding_refuses(L):
 
     for bad in (dict(), dict(K=k.half()), dict(K=k[:, :, :32]), dict(V=k[:5]), dict(q_off=off.long()),
                 dict(kv_off=torch.tensor([0, 1, 9], dtype=torch.int32)), dict(O=torch.zeros(6, 4, 32)),
-                dict(Q=q.transpose(0, 1)), dict(lse=torch.zeros(6, 4, dtype=torch.float64)),
+                dict(Q=q.transpose(0, 1)), dict(K=k[:1].expand(9, 2, 64)), dict(lse=torch.zeros(6, 4, dtype=torch.float64)),
                 dict(kv_lens=torch.zeros(2, dtype=torch.int32)), dict(O=torch.zeros(6, 64, 4).transpose(1, 2))):
         with pytest.raises(ValueError):  # the first one: nothing wrong but the device
             forward(**bad)
