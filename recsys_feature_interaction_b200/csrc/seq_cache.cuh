@@ -69,22 +69,18 @@ __global__ void __launch_bounds__(SEQ_COPY_THREADS)
   }
   const int64_t row = on ? seq_cache_row(a, p.b, p.h, static_cast<int64_t>(kv.len) - q.len + i) : -1;
   if constexpr (Q8) {
-    float amax = 0.f;
-    uint32_t odd = 0;
+    // the largest magnitude as 16-bit integers, two at a time: without their signs floats order as
+    // integers do, infinities and NaN behind all others
+    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < CH; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t v = reinterpret_cast<const uint32_t*>(&x[j])[k];
-        const float lo = fabsf(Half16<T>::lo(v)), hi = fabsf(Half16<T>::hi(v));
-        odd |= !(lo < INFINITY) | !(hi < INFINITY);  // a maximum would drop a NaN
-        amax = fmaxf(amax, fmaxf(lo, hi));
-      }
+      for (int k = 0; k < 4; ++k) top = __vmaxu2(top, reinterpret_cast<const uint32_t*>(&x[j])[k] & 0x7FFF7FFFu);
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      odd |= __shfl_xor_sync(0xffffffffu, odd, o);
-    }
+    for (int o = 1; o < 4; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = max(top & 0xFFFFu, top >> 16);
+    const bool odd = top >= (Half16<T>::kBF16 ? 0x7F80u : 0x7C00u);
+    const float amax = Half16<T>::lo(top);
     // amax = 1.f * 2^(E - 127): the least e with amax <= 448 * 2^(e - 127) = 1.75 * 2^(e + 8 - 127)
     const uint32_t bits = __float_as_uint(amax);
     const int e = odd ? 255 : max(0, static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0));
