@@ -304,9 +304,6 @@ struct SeqNote {
 template <int R, int D>
 struct SeqSlots {
   static constexpr int64_t kFloats = static_cast<int64_t>(R) * (D + 2);
-  static constexpr int64_t bytes(int64_t pieces) {
-    return pieces * static_cast<int64_t>(sizeof(SeqNote)) + 2 * pieces * kFloats * 4;
-  }
   static __device__ __forceinline__ SeqNote* note(float* ws, int64_t piece) {
     return reinterpret_cast<SeqNote*>(ws) + piece;
   }

@@ -64,8 +64,6 @@ __device__ __forceinline__ uint32_t seq_raw2(uint32_t w) {
   return Half16<T>::kBF16 ? ((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u))
                           : ((w & 0x80008000u) | ((w >> 1) & 0x3F803F80u));
 }
-template <typename T>
-constexpr int kRawPow = Half16<T>::kBF16 ? 120 : 8;
 
 // Two e4m3 values as two fp16 values.
 __device__ __forceinline__ uint32_t seq_e4m3_f16(uint16_t w) {
@@ -166,11 +164,11 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
             top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[q][s][i])), fabsf(bf16_hi(qf[q][s][i]))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // top = 1.f * 2^(e - 127): times 2^(141 - e) it lies in [2^14, 2^15)
-        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        const bool plain = e < 15 || e > 254;  // nothing to scale, or not finite
-        const float f = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-        const float back = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+        // top = 1.f * 2^(e - 127): times 2^(141 - e) it lies in [2^14, 2^15). The factor stops at 2^127
+        // for the smallest; rows that are not finite stay so under any.
+        const int e = max(14, min(254, static_cast<int>(__float_as_uint(top) >> 23)));
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+        const float back = seq_pow(e - 14);  // 2^(e - 141)
 #pragma unroll
         for (int s = 0; s < C::KSTEPS; ++s)
 #pragma unroll

@@ -449,6 +449,19 @@ def test_small_values_of_8_bit_rows(d, n, dt):
 
 
 @pytest.mark.parametrize("n", [1, 70])
+def test_the_smallest_queries_over_the_largest_keys(n):
+    """Queries near the type's smallest normal value, 8-bit keys with exponents to match: ordinary scores."""
+    gen = torch.Generator().manual_seed(12)
+    c = Cached([300, 40], 1, 64, "bf16", 16, 8)
+    c.cache["K_exp"] += 115
+    q = _rand(gen, c.dt, n + 1, 2, 64).float() * 2.0 ** -116
+    q = torch.where(q.abs() < 2.0 ** -122, 0.0, q).to(c.dt)
+    O, L = _attend(c, q, U.offsets([n, 1]), n, True)
+    _ok()
+    _check_attend(c, q, [n, 1], O, L, True)
+
+
+@pytest.mark.parametrize("n", [1, 70])
 def test_a_row_that_is_not_finite_shows(n):
     """A NaN row that takes part makes the rows that see it NaN, and no others."""
     gen = torch.Generator().manual_seed(1)
