@@ -507,8 +507,9 @@ WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_wha
  *
  * and lse[i] = log sum_j exp S[i, j]. A row that sees no key has O = 0 and lse = -inf, and its
  * gradients are 0. Rows of tensors behind the last boundary are neither read into a result nor
- * written, whatever they hold; neither are rows of one sequence into the result of another. (Inside a sequence an infinite or NaN
- * value row may show in rows that a causal mask hides it from: their weights for it are 0.)
+ * written, whatever they hold; neither are rows of one sequence into the result of another.
+ * (Inside a sequence an infinite or NaN value row may show in rows that a causal mask hides it from:
+ * their weights for it are 0.)
  *
  * Offsets, lengths and page tables are on the device, so their content is checked there: where they
  * point outside the tensors, or a sequence is longer than max_q / max_kv says, the access is
@@ -541,11 +542,11 @@ WK_API wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, in
 /* O [total_q, q_heads, d] and, unless NULL, lse [total_q, q_heads] fp32 of Q [total_q, q_heads, d]
  * over K, V [total_kv, kv_heads, d]. q_off, kv_off: batch + 1 offsets. kv_lens: batch lengths, of
  * sequence b's rows the first kv_lens[b] are keys (padded batches: kv_off[b] = b * L), or NULL:
- * all are. V may be K (shared keys and values). O must not overlap Q, K or V. Pointers 16-byte
- * aligned, the offsets 4-byte. Asynchronous on `stream`; may be captured. Errors:
- * WK_ERR_INVALID_ARG (NULL, misaligned, negative or inconsistent sizes, workspace too small,
- * O overlapping an input or the workspace), WK_ERR_UNSUPPORTED (d, dtype, a stride that is no multiple of 8),
- * WK_ERR_CUDA. */
+ * all are. V may be K (shared keys and values). O, lse and the workspace must not overlap the
+ * inputs or one another. Pointers 16-byte aligned, the offsets 4-byte. Asynchronous on `stream`;
+ * may be captured. Errors: WK_ERR_INVALID_ARG (NULL, misaligned, negative or inconsistent sizes,
+ * workspace too small, overlapping buffers), WK_ERR_UNSUPPORTED (d, dtype, a stride that is no
+ * multiple of 8), WK_ERR_CUDA. */
 WK_API wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void* K, const void* V,
                                   const int32_t* q_off, const int32_t* kv_off, const int32_t* kv_lens, void* O,
                                   float* lse, void* workspace, int64_t workspace_bytes, wk_stream_t stream);
@@ -583,8 +584,8 @@ typedef struct {
  * LAST ones of its kv_lens[b] positions (kv_lens counts them). table [batch, table_width] int32.
  * A 16-bit cache takes tokens of its own type. Two tokens must not go to one place (a page that two
  * sequences append to): what that row then holds is one of the two, or a mix. Entries of the table
- * that no new token needs are not read. The cache's K and V and the tokens must not overlap. Errors: WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED (d,
- * page_size, dtypes), WK_ERR_CUDA. */
+ * that no new token needs are not read. The cache's tensors and the tokens must not overlap. Errors:
+ * WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED (d, page_size, dtypes), WK_ERR_CUDA. */
 WK_API wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, int64_t k_stride,
                                 int64_t v_stride, wk_dtype dtype, const int32_t* new_off, const int32_t* table,
                                 int32_t table_width, const int32_t* kv_lens, int32_t batch, int64_t total_new,

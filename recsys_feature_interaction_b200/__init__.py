@@ -618,17 +618,25 @@ def wk_whale_fusion_ffn(Hw, A, weights, Hf, rows, d, h, dtype, eps=0.0, stream=N
 _torch = None
 
 
-def _int32(t, name, *shape):
-    """Address of dense int32 data of the given sizes (None: any size)."""
+def _int32(t, name, n):
+    """Address of n dense int32 values (None: any number)."""
     if t is None:
         return None
-    have = t.shape
-    if t.dtype is not _torch.int32 or len(have) != len(shape) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor of %d dimensions" % (name, len(shape)))
-    for x, want in zip(have, shape):
-        if want is not None and x != want:
-            raise ValueError("%s has shape %s, expected %s" % (name, tuple(have), shape))
+    if t.dtype is not _torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of one dimension" % name)
+    if n is not None and t.numel() != n:
+        raise ValueError("%s has %d values, expected %d" % (name, t.numel(), n))
     return t.data_ptr()
+
+
+def _table(t, batch):
+    """(address, width) of a [batch, width] page table."""
+    if t.dtype is not _torch.int32 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("the table must be a contiguous int32 tensor of two dimensions")
+    n, width = t.shape
+    if n != batch:
+        raise ValueError("the table has %d rows, expected %d" % (n, batch))
+    return t.data_ptr(), width
 
 
 def _tokens(t, name):
@@ -661,9 +669,11 @@ def _call(name, args, stream, tensors):
     """Calls lib().<name>(*args, stream) with the tensors' device as the current one."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError("%s takes tensors of one CUDA device, got %s"
-                             % (name, sorted({str(t.device) for t in tensors if t is not None})))
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError("%s takes tensors of one CUDA device, got %s"
+                         % (name, sorted({str(t.device) for t in tensors if t is not None})))
     if stream is None:
         stream = _torch._C._cuda_getCurrentRawStream(dev)
     elif not isinstance(stream, int):
@@ -748,21 +758,21 @@ def _cache(cache):
     _ready()
     K, V, ke, ve = cache["K"], cache["V"], cache.get("K_exp"), cache.get("V_exp")
     shape, dtype = K.shape, K.dtype
-    if len(shape) != 4 or V.shape != shape or V.dtype is not dtype or not K.is_contiguous() or not V.is_contiguous():
+    if len(shape) != 4 or V.shape != shape or V.dtype is not dtype or not (K.is_contiguous() and V.is_contiguous()):
         raise ValueError("a cache's K and V must be contiguous [pages, kv_heads, page_size, d] tensors of one type")
-    eight = dtype is _torch.float8_e4m3fn or dtype is _torch.uint8
-    if not eight and K.element_size() == 1:
-        raise ValueError("an 8-bit cache holds e4m3 values")
-    if (ke is not None) != eight or (ve is not None) != eight:
-        raise ValueError("K_exp and V_exp belong to 8-bit caches, and to those only")
     pages, heads, page, d = shape
-    if eight:
-        for t in (ke, ve):
-            if t.dtype is not _torch.uint8 or t.shape != shape[:3] or not t.is_contiguous():
-                raise ValueError("K_exp and V_exp must be contiguous uint8 [pages, kv_heads, page_size]")
-        return (WkCache(K.data_ptr(), V.data_ptr(), ke.data_ptr(), ve.data_ptr(), pages, page, heads, d, WK_E4M3),
-                (K, V, ke, ve))
-    return WkCache(K.data_ptr(), V.data_ptr(), None, None, pages, page, heads, d, _code16(dtype)), (K, V)
+    if ke is None and ve is None:
+        if K.element_size() == 1:
+            raise ValueError("an 8-bit cache has K_exp and V_exp")
+        return WkCache(K.data_ptr(), V.data_ptr(), None, None, pages, page, heads, d, _code16(dtype)), (K, V)
+    if ke is None or ve is None or (dtype is not _torch.float8_e4m3fn and dtype is not _torch.uint8):
+        raise ValueError("K_exp and V_exp belong to caches of e4m3 values, and to those only")
+    rows = shape[:3]
+    if not (ke.dtype is _torch.uint8 and ve.dtype is _torch.uint8 and ke.shape == rows and ve.shape == rows
+            and ke.is_contiguous() and ve.is_contiguous()):
+        raise ValueError("K_exp and V_exp must be contiguous uint8 [pages, kv_heads, page_size]")
+    return (WkCache(K.data_ptr(), V.data_ptr(), ke.data_ptr(), ve.data_ptr(), pages, page, heads, d, WK_E4M3),
+            (K, V, ke, ve))
 
 
 def wk_cache_write(cache, K, V, new_off, table, kv_lens, max_new, stream=None):
@@ -775,7 +785,7 @@ def wk_cache_write(cache, K, V, new_off, table, kv_lens, max_new, stream=None):
         raise ValueError("K, V and the cache disagree")
     batch = new_off.shape[0] - 1
     args = [ctypes.byref(c), K.data_ptr(), V.data_ptr(), ks, vs, _code16(K.dtype), _int32(new_off, "new_off", None),
-            _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch), batch, n,
+            *_table(table, batch), _int32(kv_lens, "kv_lens", batch), batch, n,
             int(max_new)]
     _call("wk_cache_write", args, stream, (K, V, new_off, table, kv_lens, *held))
 
@@ -786,7 +796,7 @@ def wk_cache_read(cache, table, kv_lens, out_off, K, V, max_kv, stream=None):
     batch = out_off.shape[0] - 1
     if K.dim() != 3 or K.shape[1:] != held[0].shape[1::2]:
         raise ValueError("K must be [tokens, kv_heads, d] of the cache")
-    args = [ctypes.byref(c), _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
+    args = [ctypes.byref(c), *_table(table, batch), _int32(kv_lens, "kv_lens", batch),
             _int32(out_off, "out_off", None), _dense(K, "K", K.shape, K.dtype), _dense(V, "V", K.shape, K.dtype),
             _code16(K.dtype), batch, K.shape[0], int(max_kv)]
     _call("wk_cache_read", args, stream, (K, V, out_off, table, kv_lens, *held))
@@ -815,7 +825,7 @@ def wk_cache_attention(cache, Q, O, q_off, table, kv_lens, max_q, max_kv, causal
     batch = q_off.shape[0] - 1
     cfg = _cache_config(c, Q, batch, max_q, max_kv, scale)
     args = [ctypes.byref(c), ctypes.byref(cfg), Q.data_ptr(), _int32(q_off, "q_off", None),
-            _int32(table, "table", batch, None), table.shape[1], _int32(kv_lens, "kv_lens", batch),
+            *_table(table, batch), _int32(kv_lens, "kv_lens", batch),
             1 if causal else 0, _dense(O, "O", Q.shape, Q.dtype), _dense(lse, "lse", Q.shape[:2], _torch.float32),
             *_scratch(workspace)]
     _call("wk_cache_attention", args, stream, (Q, O, q_off, table, kv_lens, lse, workspace, *held))

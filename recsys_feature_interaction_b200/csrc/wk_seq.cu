@@ -35,15 +35,32 @@ int64_t extent(int64_t rows, int64_t stride, int heads, int d) {
   return rows <= 0 ? 0 : ((rows - 1) * stride + static_cast<int64_t>(heads) * d) * 2;
 }
 
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-  const uint8_t *x = static_cast<const uint8_t*>(a), *y = static_cast<const uint8_t*>(b);
-  return an > 0 && bn > 0 && x && y && x < y + bn && y < x + an;
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+
+// Whether something written lies over something read, or over something else written.
+template <int W, int R>
+bool overlap(const Bytes (&written)[W], const Bytes (&read)[R]) {
+  auto over = [](const Bytes& a, const Bytes& b) {
+    const uint8_t *x = static_cast<const uint8_t*>(a.p), *y = static_cast<const uint8_t*>(b.p);
+    return a.n > 0 && b.n > 0 && x && y && x < y + b.n && y < x + a.n;
+  };
+  for (int i = 0; i < W; ++i) {
+    for (const Bytes& r : read)
+      if (over(written[i], r)) return true;
+    for (int j = 0; j < i; ++j)
+      if (over(written[i], written[j])) return true;
+  }
+  return false;
 }
 
 wk_status check_config(const wk_xattn_config* c) {
   if (!c || c->batch < 0 || c->q_heads < 1 || c->kv_heads < 1 || c->q_heads % c->kv_heads != 0 || c->max_q < 0 ||
       c->max_kv < 0 || c->total_q < 0 || c->total_kv < 0 || c->total_q > kMaxRows || c->total_kv > kMaxRows ||
-      c->max_kv > kMostRows || static_cast<int64_t>(c->max_q) * c->q_heads > kMostRows || !(c->scale >= 0.f) || !std::isfinite(c->scale))
+      c->max_kv > kMostRows || static_cast<int64_t>(c->max_q) * c->q_heads > kMostRows || !(c->scale >= 0.f) ||
+      !std::isfinite(c->scale))
     return WK_ERR_INVALID_ARG;
   if (!seq_d_ok(c->d) || !type16(c->dtype) || c->q_heads > 1024 || c->q_heads / c->kv_heads > 64)
     return WK_ERR_UNSUPPORTED;
@@ -69,10 +86,9 @@ wk_status check_cache(const wk_cache* c) {
   return WK_OK;
 }
 
-// Bytes of a cache's K (or V).
-int64_t cache_bytes(const wk_cache& c) {
-  return static_cast<int64_t>(c.num_pages) * c.kv_heads * c.page_size * c.d * (c.dtype == WK_E4M3 ? 1 : 2);
-}
+// Rows of a cache, and bytes of its K (or V).
+int64_t cache_rows(const wk_cache& c) { return static_cast<int64_t>(c.num_pages) * c.kv_heads * c.page_size; }
+int64_t cache_bytes(const wk_cache& c) { return cache_rows(c) * c.d * (c.dtype == WK_E4M3 ? 1 : 2); }
 
 int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
@@ -403,12 +419,13 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
   if (s != WK_OK) return s;
   if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;
   SeqArgs a = make_args(*cfg, q_off, kv_off, kv_lens, nullptr);
-  const int64_t ob = extent(cfg->total_q, static_cast<int64_t>(cfg->q_heads) * cfg->d, cfg->q_heads, cfg->d);
-  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)) ||
-      overlap(O, ob, K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)) ||
-      overlap(O, ob, V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)) ||
-      overlap(O, ob, workspace, need) || overlap(O, ob, lse, cfg->total_q * cfg->q_heads * 4))
-    return WK_ERR_INVALID_ARG;
+  const Bytes written[] = {{O, cfg->total_q * cfg->q_heads * cfg->d * 2},
+                           {lse, cfg->total_q * cfg->q_heads * 4},
+                           {workspace, need}};
+  const Bytes read[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
+                        {K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)},
+                        {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)}};
+  if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
   if (s != WK_OK) return s;
@@ -433,23 +450,15 @@ wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const voi
   if (s != WK_OK) return s;
   if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;
   SeqArgs a = make_args(*cfg, q_off, kv_off, kv_lens, nullptr);
-  // no gradient may lie over an input or another gradient
-  const int64_t qd = static_cast<int64_t>(cfg->q_heads) * cfg->d, kd = static_cast<int64_t>(cfg->kv_heads) * cfg->d;
-  const int64_t qb = cfg->total_q * qd * 2, kb = cfg->total_kv * kd * 2;
-  const struct {
-    const void* p;
-    int64_t n;
-  } in[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
-            {K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)},
-            {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)},
-            {O, qb}, {dO, qb}, {lse, cfg->total_q * cfg->q_heads * 4}, {workspace, need}},
-    out[] = {{dQ, qb}, {dK, kb}, {dV, kb}};
-  for (int i = 0; i < 3; ++i) {
-    for (const auto& x : in)
-      if (overlap(out[i].p, out[i].n, x.p, x.n)) return WK_ERR_INVALID_ARG;
-    for (int j = 0; j < i; ++j)
-      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return WK_ERR_INVALID_ARG;
-  }
+  const int64_t qb = cfg->total_q * cfg->q_heads * cfg->d * 2, kb = cfg->total_kv * cfg->kv_heads * cfg->d * 2;
+  const Bytes written[] = {{dQ, qb}, {dK, kb}, {dV, kb}, {workspace, need}};
+  const Bytes read[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
+                        {K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)},
+                        {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)},
+                        {O, qb},
+                        {dO, qb},
+                        {lse, cfg->total_q * cfg->q_heads * 4}};
+  if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   if (!rows && !keys) return WK_OK;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
@@ -477,11 +486,13 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
     return WK_ERR_INVALID_ARG;
   SeqArgs a = make_args(cfg, new_off, nullptr, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
-  const int64_t cb = cache_bytes(*cache), kb = extent(total_new, a.k_stride, cfg.kv_heads, cfg.d),
-                vb = extent(total_new, a.v_stride, cfg.kv_heads, cfg.d);
-  if (overlap(cache->K, cb, cache->V, cb) || overlap(cache->K, cb, K, kb) || overlap(cache->K, cb, V, vb) ||
-      overlap(cache->V, cb, K, kb) || overlap(cache->V, cb, V, vb))
-    return WK_ERR_INVALID_ARG;
+  const Bytes written[] = {{cache->K, cache_bytes(*cache)},
+                           {cache->V, cache_bytes(*cache)},
+                           {cache->K_exp, cache_rows(*cache)},
+                           {cache->V_exp, cache_rows(*cache)}};
+  const Bytes read[] = {{K, extent(total_new, a.k_stride, cfg.kv_heads, cfg.d)},
+                        {V, extent(total_new, a.v_stride, cfg.kv_heads, cfg.d)}};
+  if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   const int32_t chunks = (max_new + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
   const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
   if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
@@ -504,11 +515,12 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   if (!K || !V || !out_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
       !al4(out_off) || !al4(table) || !al4(kv_lens))
     return WK_ERR_INVALID_ARG;
-  const int64_t bytes = total * cache->kv_heads * cache->d * 2;
-  const int64_t cb = cache_bytes(*cache);
-  if (overlap(K, bytes, V, bytes) || overlap(K, bytes, cache->K, cb) || overlap(K, bytes, cache->V, cb) ||
-      overlap(V, bytes, cache->K, cb) || overlap(V, bytes, cache->V, cb))
-    return WK_ERR_INVALID_ARG;
+  const Bytes written[] = {{K, total * cache->kv_heads * cache->d * 2}, {V, total * cache->kv_heads * cache->d * 2}};
+  const Bytes read[] = {{cache->K, cache_bytes(*cache)},
+                        {cache->V, cache_bytes(*cache)},
+                        {cache->K_exp, cache_rows(*cache)},
+                        {cache->V_exp, cache_rows(*cache)}};
+  if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
   SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
@@ -550,12 +562,15 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   SeqArgs a = make_args(*cfg, q_off, nullptr, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
   a.causal = causal != 0;
-  const int64_t ob = cfg->total_q * cfg->q_heads * cfg->d * 2;
-  const int64_t cb = cache_bytes(*cache);
-  if (overlap(O, ob, Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)) || overlap(O, ob, workspace, need) ||
-      overlap(O, ob, lse, cfg->total_q * cfg->q_heads * 4) || overlap(O, ob, cache->K, cb) ||
-      overlap(O, ob, cache->V, cb))
-    return WK_ERR_INVALID_ARG;
+  const Bytes written[] = {{O, cfg->total_q * cfg->q_heads * cfg->d * 2},
+                           {lse, cfg->total_q * cfg->q_heads * 4},
+                           {workspace, need}};
+  const Bytes read[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
+                        {cache->K, cache_bytes(*cache)},
+                        {cache->V, cache_bytes(*cache)},
+                        {cache->K_exp, cache_rows(*cache)},
+                        {cache->V_exp, cache_rows(*cache)}};
+  if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
   if (s != WK_OK) return s;

@@ -195,6 +195,9 @@ def test_pointers_that_are_refused(L):
     assert call(a6=_far(1) + 64) == wk.WK_ERR_INVALID_ARG       # O over Q
     assert call(a6=_far(2)) == wk.WK_ERR_INVALID_ARG            # O over K
     assert call(a7=_far(4) + 16) == wk.WK_ERR_INVALID_ARG       # lse in O
+    assert call(a7=_far(1)) == wk.WK_ERR_INVALID_ARG            # lse over Q
+    assert L.wk_xattn_forward(ctypes.byref(_cfg(max_kv=5000)), *(good[:8] + [_far(2)] + good[9:])) \
+        == wk.WK_ERR_INVALID_ARG                                # the workspace over K
     assert call(a9=-1) == wk.WK_ERR_INVALID_ARG
     e = _cfg(batch=0)
     assert L.wk_xattn_forward(ctypes.byref(e), *([None] * 9), 0, None) == wk.WK_OK
@@ -214,6 +217,7 @@ def test_pointers_that_are_refused(L):
     assert grad(13, n.value - 1) == wk.WK_ERR_INVALID_ARG
     assert grad(12, None) == wk.WK_ERR_INVALID_ARG
     assert grad(9, _far(1)) == wk.WK_ERR_INVALID_ARG and grad(10, _far(3) + 256) == wk.WK_ERR_INVALID_ARG
+    assert grad(12, _far(5)) == wk.WK_ERR_INVALID_ARG           # the workspace over dO
     assert grad(11, _far(8)) == wk.WK_ERR_INVALID_ARG and grad(9, _far(10)) == wk.WK_ERR_INVALID_ARG
     for i in (0, 1, 2, 3, 4, 5, 6, 7, 9, 10, 11):
         assert grad(i, None) == wk.WK_ERR_INVALID_ARG
@@ -274,9 +278,12 @@ def test_cache_calls_that_are_refused(L):
     assert write(_cache(V=_far(1) + 64)) == wk.WK_ERR_INVALID_ARG
     assert write(q8, a0=_far(1)) == wk.WK_ERR_INVALID_ARG and write(q8, a1=_far(1) + 128) == wk.WK_ERR_INVALID_ARG
     assert L.wk_cache_read(ctypes.byref(q8), *(r[:4] + [_far(2)] + r[5:])) == wk.WK_ERR_INVALID_ARG
+    assert write(_cache(K_exp=_far(1) + 64)) == wk.WK_ERR_INVALID_ARG
     cfg = _cfg()
     att = [_far(7), FAKE, FAKE, 4, FAKE, 1, _far(8), None, _far(9), 1 << 30, None]
-    for over in (_far(7) + 32, _far(1) + 16, _far(2)):
+    assert L.wk_cache_attention(ctypes.byref(q8), ctypes.byref(cfg), *(att[:7] + [_far(7)] + att[8:])) \
+        == wk.WK_ERR_INVALID_ARG  # lse over Q
+    for over in (_far(7) + 32, _far(1) + 16, _far(2), _far(4)):
         assert L.wk_cache_attention(ctypes.byref(q8), ctypes.byref(cfg), *(att[:6] + [over] + att[7:])) \
             == wk.WK_ERR_INVALID_ARG
 
