@@ -2,16 +2,16 @@
 // 5th-generation tensor cores, over jagged tensors or a cache.
 //
 // A block holds up to 128 packed query rows (whole tokens of the query heads that share a key head)
-// and walks 128-key blocks: S = Q K^T from shared memory, softmax weights from TMEM by two warps per lane quarter,
-// P written over S's columns, O += P V with the V tile MN-major. S has two or three
-// buffers and runs one or two blocks ahead of P V; K and V tiles arrive in one ring in the order in
-// which the products use them (K0, K1, V0, K2, V1, ..).
+// and walks 128-key blocks: S = Q K^T from shared memory, softmax weights from TMEM by two groups of
+// four warps that take the blocks in turn, P written over S's columns, O += P V with the V tile
+// MN-major. S has two or three buffers and runs one or two blocks ahead of P V; K and V tiles arrive
+// in one ring in the order in which the products use them (K0, K1, V0, K2, V1, ..).
 //
-// Roles: warp 0 lane 0 loads tiles with TMA (jagged: 128 rows from the sequence's first; a 16-bit
-// cache: one box per page); warp 1 issues the MMAs; warp 2 walks the block's units and hands them
-// to the other roles through a ring, so that none of them waits for offsets; warps 4 .. 11 run the
-// softmax; for an 8-bit cache warps 12 .. 15 load rows, convert them to the 16-bit type (exactly;
-// see seq_rows.cuh) and store them in the tiles' swizzled layout, in place of the TMA.
+// Roles: warp 0 loads tiles with TMA (jagged: 128 rows from the sequence's first; a 16-bit cache:
+// one box per page, each by the lane that holds its number); warp 1 issues the MMAs; warp 2 walks the
+// block's units and hands them to the other roles through a ring, so that none of them waits for
+// offsets; warps 4 .. 11 run the softmax; for an 8-bit cache warps 12 .. 15 load rows, convert them
+// to the 16-bit type and store them in the tiles' swizzled layout, in place of the TMA.
 //
 // Rows behind a sequence's last key belong to someone else: their scores are replaced by a select,
 // and their V rows, whose weights are 0, are overwritten with zeros in the tile before P V, because

@@ -349,7 +349,10 @@ struct RunBackward {
       const wk_status s = one<D, T, true>(k, delta, slots, dK, dV);
       if (s != WK_OK) return s;
       if (a.kv_lens) {
-        return launch(seq_zero_padding_kernel<T>, dim3(static_cast<unsigned>(a.batch), 2), 256, 0, st,
+        // a block for each 16 KB that a sequence would have to clear if it were all padding
+        const int64_t each = a.total_kv / a.batch * a.kv_heads * D * 2;
+        const unsigned z = static_cast<unsigned>(std::clamp<int64_t>(each >> 14, 1, 64));
+        return launch(seq_zero_padding_kernel<T>, dim3(static_cast<unsigned>(a.batch), 2, z), 256, 0, st,
                       static_cast<T*>(dK), static_cast<T*>(dV), static_cast<int64_t>(a.kv_heads) * D, a);
       }
     }

@@ -148,6 +148,17 @@ def test_padded_batch_with_poisoned_padding(d, dt):
     j.check(O, L, grads, lens=lens)
 
 
+def test_much_padding():
+    """Far more padding than keys, an odd number of rows of it."""
+    lens = [3, 0, 1500]
+    j = Jagged([4, 2, 3], [1537, 4099, 1500], 2, 2, 160, "bf16")
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    O, L = j.forward(lens=t)
+    grads = j.backward(O, L, lens=t)
+    _ok()
+    j.check(O, L, grads, lens=lens)
+
+
 @pytest.mark.parametrize("d", [64, 160])
 def test_a_poisoned_neighbour_stays_its_own(d):
     """Sequence 1 of three holds NaN in q, k, v and dO: the others' results do not change."""
