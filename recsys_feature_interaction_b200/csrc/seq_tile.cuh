@@ -13,6 +13,14 @@
 // offsets; warps 4 .. 11 run the softmax; for an 8-bit cache warps 12 .. 15 load rows, convert them
 // to the 16-bit type and store them in the tiles' swizzled layout, in place of the TMA.
 //
+// Powers of two of 8-bit rows. bf16 has room for every one, so its tiles hold the rows' values. fp16
+// has not: its tiles hold the e4m3 values, K's power is a factor of the fp32 score, and V's is added to
+// the exponent of the weight, P = 2^(S + x - w) with w the running maximum of S + x over the keys that
+// the row sees, beside the row sum of 2^(S - m). So a row's share does not depend on what other rows
+// hold, seen or not. (With rows relative to the largest of the piece, those 2^22 below it lost bits.)
+// The second exponential costs less than the simpler conversion saves: chunks of 200 .. 512 tokens over
+// up to 4096 keys (d = 128, 8 heads on 2) take 143 us in fp16, 152 in bf16.
+//
 // Rows behind a sequence's last key belong to someone else: their scores are replaced by a select,
 // and their V rows, whose weights are 0, are overwritten with zeros in the tile before P V, because
 // 0 * NaN is NaN.
@@ -214,26 +222,33 @@ struct StCfg {
   static constexpr int TILEB = NBOX * BOXB;              // one K or V tile
   static constexpr int LIMIT = 227 * 1024;
   static constexpr int NU = 4;                           // units in flight between the walker and the roles
-  static constexpr int BARB = 512;                       // barriers, TMEM address, references
+  static constexpr int BARB = 512;                       // barriers, TMEM address
   static constexpr int UNITB = NU * static_cast<int>(sizeof(SeqUnit));
-  static constexpr int REDB = 4 * R * 4;                 // what the softmax groups tell each other, per row
+  static constexpr int REDB = (SRC == SEQ_PAGED8 ? 6 : 4) * R * 4;  // what the softmax groups tell each other, per row
   static constexpr int STAGEB = 8 * SEQ_STAGE_BYTES;     // the softmax warps' output tiles
-  static constexpr int FIXED = BARB + UNITB + REDB + STAGEB;
+  // TMEM: NS buffers of S (P over their first 64 columns), then O. With three, S runs two blocks
+  // ahead of P V, and a softmax group finds its next block ready; d = 160 has room for two.
+  static constexpr int NS = D <= 128 ? 3 : 2;
+  static constexpr int AHEAD = NS - 1;
+  // Powers of two of a block's key and value rows (fp16 over an 8-bit cache), for NX blocks: written
+  // with K's tile, read by the softmax warps. Between the tile of V of block g - NX and that of K of
+  // block g the ring takes at least 2 (NX - AHEAD - 1) others, so a loader that has found room for the
+  // latter knows that the former's product, and the softmax before it, are done.
+  static constexpr int NX = AHEAD == 2 ? 8 : 4;
+  static constexpr int COLB = SRC == SEQ_PAGED8 ? NX * 2 * KB * 4 : 0;
+  static constexpr int FIXED = BARB + UNITB + REDB + STAGEB + COLB;
   // one Q tile: the next unit's is loaded once this one's last S is done, under its last blocks
   static constexpr int STAGES_RAW = (LIMIT - FIXED - TILEB) / TILEB;
   static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
   // more than half an SM's shared memory: one block per SM, whose 512 TMEM columns are its own
   static constexpr int RAW = FIXED + (1 + STAGES) * TILEB;
   static constexpr int SMEM = RAW > 120 * 1024 ? RAW : 120 * 1024;
-  // TMEM: NS buffers of S (P over their first 64 columns), then O. With three, S runs two blocks
-  // ahead of P V, and a softmax group finds its next block ready; d = 160 has room for two.
-  static constexpr int NS = D <= 128 ? 3 : 2;
-  static constexpr int AHEAD = NS - 1;
   static constexpr int OCOL = NS * KB;
   static constexpr int THREADS = SRC == SEQ_PAGED8 ? 512 : 384;
   static constexpr int LOADERS = 128;
   static_assert(OCOL + D <= 512 && STAGES >= 4 && TILEB % 1024 == 0 && UNITB % 16 == 0, "layout");
-  static_assert((2 * STAGES + 4 * NS + 2 + 2 + 2 * NU) * 8 + 16 + NU * 8 + 32 <= BARB, "barriers");
+  static_assert((2 * STAGES + 4 * NS + 2 + 2 + 2 * NU) * 8 + 16 <= BARB, "barriers");
+  static_assert(2 * (NX - AHEAD - 1) + 1 >= STAGES, "powers of two are overwritten only after use");
 };
 
 // Key blocks [j0, j1) of a unit that hold keys (a unit without keys has a cost, but no block).
@@ -249,6 +264,10 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
                     T* __restrict__ O, float* __restrict__ lse, float* __restrict__ ws, SeqArgs a, int64_t pieces) {
   using C = StCfg<D, SRC>;
   constexpr int R = C::R, KB = C::KB;
+  // fp16 over an 8-bit cache: fp16 cannot hold every power of two, so the tiles hold the e4m3 values
+  // and the rows' powers join the fp32 scores (K) and the exponents of the weights (V). bf16 tiles
+  // hold the rows' values themselves.
+  constexpr bool FAR = SRC == SEQ_PAGED8 && !Half16<T>::kBF16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   if ((smem_u32(smem_raw) & 1023u) != 0u) {  // the swizzled layout needs 1024-byte alignment
     if (threadIdx.x == 0) flag_error(a.status, kFlagBadShape);
@@ -269,10 +288,9 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
   uint64_t* u_full = q_empty + 1;            // [NU] unit handed over
   uint64_t* u_empty = u_full + C::NU;        // [NU] every role is done with it
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(u_empty + C::NU);
-  int32_t* refs = reinterpret_cast<int32_t*>(tmem_slot + 4);  // [NU][2] exponent references of K and V
   SeqUnit* unit = reinterpret_cast<SeqUnit*>(tiles + C::STAGES * C::TILEB + C::BARB);
   float* red = reinterpret_cast<float*>(tiles + C::STAGES * C::TILEB + C::BARB + C::UNITB);
-  int32_t* shared_top = refs + 2 * C::NU;                // [2][4] the loaders' maxima
+  float* columns = red + (C::REDB + C::STAGEB) / 4;      // [NX][2][KB] a block's powers of two
   unsigned* status = a.status;
 
   const int warp = threadIdx.x >> 5;
@@ -550,6 +568,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     const int pair_id = 1 + q, hear_id = 6 + q + 4 * (grp ^ 1), tell_id = 6 + q + 4 * grp;
     float* mrow = red;           // [2][R] running maximum after a group's last block
     float* lrow = red + 2 * R;   // [2][R] row sums at the end of a unit, relative to mrow
+    float* wrow = red + 4 * R;   // [2][R] FAR: as mrow, of the scores plus V's exponents
     uint8_t* stage = reinterpret_cast<uint8_t*>(red) + C::REDB + (warp - 4) * SEQ_STAGE_BYTES;
     uint32_t g = 0;
     // After a failed wait a thread stops waiting but walks the unit to its end, so that the
@@ -571,14 +590,15 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       const int64_t orow = (u.q_begin + qi) * a.q_heads + qh;
       if (u.j0 < j1) {
         float m = -INFINITY, l = 0.f;  // this group's row sum, relative to m
+        float wm = -INFINITY;          // FAR: what the weights are relative to
         for (int j = u.j0; j < j1; ++j, ++g) {
           if ((g & 1u) != static_cast<uint32_t>(grp)) continue;
           const uint32_t buf = g % C::NS;
           if (ok) ok = seq_wait(&s_full[buf], (g / C::NS) & 1u, status);
           tc_fence_after();
-          float scale_log2 = a.scale * 1.4426950408889634f;
-          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
-            scale_log2 *= seq_ex2(static_cast<float>(refs[2 * (ui % C::NU)] - 127));
+          const float scale_log2 = FAR ? 1.f : a.scale * 1.4426950408889634f;  // FAR: part of K's factors
+          const float* kfac = columns + (g % C::NX) * 2 * KB;
+          const float* vexp = kfac + KB;
           // Half of the block's scores at a time: the second half's maximum, the first half's, then the
           // first half's weights, and the second half again (a whole row would not fit the registers).
           uint32_t sr[KB / 2];
@@ -591,28 +611,51 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
               tmem_ld32(ta + at + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
               tmem_ld_wait();
             }
+            if constexpr (FAR) {
+#pragma unroll
+              for (int c4 = 0; c4 < KB / 8; ++c4) {
+                const float4 f = *reinterpret_cast<const float4*>(kfac + at + 4 * c4);
+                const float fv[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  sr[4 * c4 + i] = __float_as_uint(__uint_as_float(sr[4 * c4 + i]) * fv[i]);
+              }
+            }
             if (!full) {
 #pragma unroll
               for (int c = 0; c < KB / 2; ++c)
                 if (at + c >= kvalid) sr[c] = 0xFF800000u;  // -inf
             }
           };
-          float mh = -INFINITY;
+          float mh = -INFINITY, wh = -INFINITY;
 #pragma unroll 1
           for (int at = KB / 2; at >= 0; at -= KB / 2) {
             load_half(at);
             mh = seq_max2(mh, seq_max<KB / 2>(sr));
+            if constexpr (FAR) {
+#pragma unroll
+              for (int c4 = 0; c4 < KB / 8; ++c4) {
+                const float4 x = *reinterpret_cast<const float4*>(vexp + at + 4 * c4);
+                wh = seq_max3(wh, __uint_as_float(sr[4 * c4]) + x.x, __uint_as_float(sr[4 * c4 + 1]) + x.y);
+                wh = seq_max3(wh, __uint_as_float(sr[4 * c4 + 2]) + x.z, __uint_as_float(sr[4 * c4 + 3]) + x.w);
+              }
+            }
           }
-          float mprev = -INFINITY;
+          float mprev = -INFINITY, wprev = -INFINITY;
           if (j > u.j0) {
             named_bar(hear_id, 64);
             mprev = mrow[(grp ^ 1) * R + row];
+            if constexpr (FAR) wprev = wrow[(grp ^ 1) * R + row];
           }
           const float mb2 = mh * scale_log2;
-          const bool need = row_on && mb2 > mprev + 8.f;
-          const float mnew = need ? mb2 : mprev;
+          const bool more = row_on && mb2 > mprev + 8.f;
+          const float mnew = more ? mb2 : mprev;
+          // what P and O are relative to: the running maximum, or (FAR) that of the weights' exponents
+          const bool need = FAR ? row_on && wh > wprev + 8.f : more;
+          const float wnew = FAR ? (need ? wh : wprev) : mnew;
           if (j + 1 < j1) {
             mrow[grp * R + row] = mnew;
+            if constexpr (FAR) wrow[grp * R + row] = wnew;
             named_bar_arrive(tell_id, 64);
           }
           if (j > u.j0 && __any_sync(0xffffffffu, need)) {
@@ -620,7 +663,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             const uint32_t gp = g - 1u;
             if (ok) ok = seq_wait(&p_empty[gp % C::NS], (gp / C::NS) & 1u, status);
             tc_fence_after();
-            const float factor = need ? whale_ex2(mprev - mnew) : 1.f;
+            const float factor = need ? whale_ex2((FAR ? wprev : mprev) - wnew) : 1.f;
             if (warp_on) {
 #pragma unroll 1
               for (int cc = 0; cc < D / 16; ++cc) {
@@ -636,12 +679,25 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           // P = 2^(S scale_log2 - m), rounded to the operand type over S's first 64 columns; row sum
           // in fp32
           const float nm = mnew == -INFINITY ? 0.f : -mnew;
+          const float nw = wnew == -INFINITY ? 0.f : -wnew;
           const float2 sc = make_float2(scale_log2, scale_log2), nm2 = make_float2(nm, nm);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
           for (int at = 0; at < KB; at += KB / 2) {
             if (at) load_half(at);
             uint32_t pk[KB / 4];
+            if constexpr (FAR) {  // the row sum of 2^(S - m), and P = 2^(S + V's exponent - w)
+#pragma unroll
+              for (int c4 = 0; c4 < KB / 8; ++c4) {
+                const float4 x = *reinterpret_cast<const float4*>(vexp + at + 4 * c4);
+                const float s[4] = {__uint_as_float(sr[4 * c4]), __uint_as_float(sr[4 * c4 + 1]),
+                                    __uint_as_float(sr[4 * c4 + 2]), __uint_as_float(sr[4 * c4 + 3])};
+                sum[0] = seq_add2(sum[0], make_float2(whale_ex2(s[0] + nm), whale_ex2(s[1] + nm)));
+                sum[1] = seq_add2(sum[1], make_float2(whale_ex2(s[2] + nm), whale_ex2(s[3] + nm)));
+                pk[2 * c4] = Half16<T>::pack2(whale_ex2(s[0] + (x.x + nw)), whale_ex2(s[1] + (x.y + nw)));
+                pk[2 * c4 + 1] = Half16<T>::pack2(whale_ex2(s[2] + (x.z + nw)), whale_ex2(s[3] + (x.w + nw)));
+              }
+            } else
 #pragma unroll
             for (int c2 = 0; c2 < KB / 4; ++c2) {
               const float2 x =
@@ -661,14 +717,23 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           if (mh != mh) lsum = mh;            // a NaN score: the polynomial would lose it
           l = (m == -INFINITY ? l * 0.f : l * whale_ex2(m - mnew)) + lsum;
           m = mnew;
+          wm = wnew;
         }
         // both groups' row sums, relative to the last block's maximum
         const uint32_t gl = g - 1u;
         lrow[grp * R + row] = l;
         mrow[grp * R + row] = m;
+        if constexpr (FAR) wrow[grp * R + row] = wm;
         named_bar(pair_id, 64);
         const float mf = mrow[(gl & 1u) * R + row];  // the group of the last block knows the final one
         const float mz = mf == -INFINITY ? 0.f : mf;
+        // FAR: O is relative to 2^wf and the row sum to 2^mf; the square root of what lies between them,
+        // which fp32 holds whatever V's exponents are
+        float between = 1.f;
+        if constexpr (FAR) {
+          const float wf = wrow[(gl & 1u) * R + row];
+          between = wf == -INFINITY ? 0.f : whale_ex2(0.5f * (wf - mz));
+        }
         float lt = 0.f;
 #pragma unroll
         for (int x = 0; x < 2; ++x) lt += lrow[x * R + row] * whale_ex2(mrow[x * R + row] - mz);
@@ -676,10 +741,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         if (ok) ok = seq_wait(&p_empty[gl % C::NS], (gl / C::NS) & 1u, status);
         tc_fence_after();
         if (warp_on) {
-          float vs = 1.f;  // V's reference exponent
-          if (SRC == SEQ_PAGED8 && !Half16<T>::kBF16)
-            vs = seq_ex2(static_cast<float>(refs[2 * (ui % C::NU) + 1] - 127));
-          const float inv = whole ? (lt == 0.f ? 0.f : vs / lt) : vs;
+          const float inv = between * (whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f);
           const SeqRowsOut out(orow, row_on && ok);
           using S = SeqSlots<R, D>;
           float* slot = whole ? nullptr : S::slot(ws, pieces, blockIdx.x, u.j0 > 0);
@@ -688,6 +750,10 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::OCOL + cc * 32, o);
             tmem_ld_wait();
+            if constexpr (FAR) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * between);
+            }
             if (whole) {
               seq_store_rows<D, T>(stage, o, inv, O, cc * 32, out);
             } else if (row_on && ok) {
@@ -726,7 +792,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
     const int tid = threadIdx.x - 384;
     const int pmask = (1 << a.page_shift) - 1;
     int s = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, gk = 0;  // gk: K tiles so far, the numbers that the softmax warps give their blocks
     bool ok = true;
     SeqUnit u;
     auto row_of = [&](const int32_t* trow, int k) -> int64_t {
@@ -743,43 +809,20 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
       __syncwarp();
       const int j1 = seq_real_end(a, u, group, a.tile, KB);
       const int32_t* trow = a.table + static_cast<int64_t>(u.b) * a.table_width;
-      int ref[2] = {127, 127};
-      if (!Half16<T>::kBF16 && u.j0 < j1) {
-        // fp16 cannot hold every power of two: rows are held relative to 2^7 below the piece's
-        // largest, which keeps all within 2^22 of it exact
-        int top[2] = {0, 0};
-        for (int k = u.j0 * KB + 16 * tid; k < min(u.len, j1 * KB); k += 16 * C::LOADERS) {
-          const int64_t r = row_of(trow, k);
-          if (r < 0) continue;
-          const uint4 e[2] = {__ldg(reinterpret_cast<const uint4*>(a.k_exp + r)),
-                              __ldg(reinterpret_cast<const uint4*>(a.v_exp + r))};
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int x = (reinterpret_cast<const uint32_t*>(&e[w])[i / 4] >> (8 * (i % 4))) & 255;
-              if (k + i < u.len && x != 255) top[w] = max(top[w], x);
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          top[w] = __reduce_max_sync(0xffffffffu, top[w]);
-          if (lane == 0) shared_top[w * 4 + (warp & 3)] = top[w];
-        }
-        named_bar(5, C::LOADERS);
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          ref[w] = max(max(shared_top[w * 4], shared_top[w * 4 + 1]), max(shared_top[w * 4 + 2], shared_top[w * 4 + 3])) - 7;
-        if (tid == 0) {
-          refs[2 * (ui % C::NU)] = ref[0];
-          refs[2 * (ui % C::NU) + 1] = ref[1];
-        }
-        named_bar(5, C::LOADERS);  // before the next unit's maxima
-      }
-      auto load = [&](const uint8_t* base, const uint8_t* ex, int rf, int j) {
+      auto load = [&](int which, int j) {
+        const uint8_t* base = static_cast<const uint8_t*>(which ? V8 : K8);
+        const uint8_t* ex = which ? a.v_exp : a.k_exp;
         uint4 x[ITEMS];
         uint32_t e[ITEMS];
         const int valid = min(KB, u.len - j * KB);
+        float kf = 0.f, vx = 0.f;  // FAR: the powers of two of row tid
+        if (FAR && which == 0 && tid < valid) {
+          const int64_t r = row_of(trow, j * KB + tid);
+          if (r >= 0) {
+            kf = seq_pow(__ldg(a.k_exp + r)) * (a.scale * 1.4426950408889634f);
+            vx = static_cast<float>(static_cast<int>(__ldg(a.v_exp + r)) - 127);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
           const int it = i * C::LOADERS + tid, rr = it / ITEMS, ch = it % ITEMS;
@@ -794,30 +837,38 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           }
         }
         if (ok) ok = seq_wait(&kv_empty[s], ph ^ 1u, status);
+        if (FAR && which == 0) {
+          float* col = columns + (gk++ % C::NX) * 2 * KB;
+          col[tid] = kf;
+          col[KB + tid] = vx;
+        }
         uint8_t* dst = tiles + s * C::TILEB;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
           const int it = i * C::LOADERS + tid, rr = it / ITEMS, ch = it % ITEMS;
-          uint32_t f2;
-          if constexpr (Half16<T>::kBF16) {
-            const float f = seq_pow(e[i]);
-            f2 = Half16<T>::pack2(f, f);
-          } else {
-            const float f = e[i] == 255 ? __uint_as_float(0x7FC00000u)
-                                        : seq_ex2(static_cast<float>(max(static_cast<int>(e[i]) - rf, -60) + 8));
-            f2 = Half16<T>::pack2(f, f);
-          }
           uint32_t v[8];
+          if constexpr (FAR) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t b = reinterpret_cast<const uint32_t*>(&x[i])[w];
-            v[2 * w] = seq_raw2<T>(__byte_perm(b, 0u, 0x1404));      // bytes 0, 1 at places 1, 3
-            v[2 * w + 1] = seq_raw2<T>(__byte_perm(b, 0u, 0x3424));  // bytes 2, 3
-          }
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t b = reinterpret_cast<const uint32_t*>(&x[i])[w];
+              v[2 * w] = seq_e4m3_f16(seq_lo16(b));
+              v[2 * w + 1] = seq_e4m3_f16(seq_hi16(b));
+            }
+            if (which == 1 && e[i] == 255) {  // a row that is not finite (K's shows by its factor)
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            if constexpr (Half16<T>::kBF16) v[w] = seq_mul2<T>(v[w], 0x7B807B80u);
-            v[w] = seq_mul2<T>(v[w], f2);
+              for (int w = 0; w < 8; ++w) v[w] = 0x7FFF7FFFu;
+            }
+          } else {
+            const float f = seq_pow(e[i]);
+            const uint32_t f2 = Half16<T>::pack2(f, f);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t b = reinterpret_cast<const uint32_t*>(&x[i])[w];
+              v[2 * w] = seq_raw2<T>(__byte_perm(b, 0u, 0x1404));      // bytes 0, 1 at places 1, 3
+              v[2 * w + 1] = seq_raw2<T>(__byte_perm(b, 0u, 0x3424));  // bytes 2, 3
+            }
+#pragma unroll
+            for (int w = 0; w < 8; ++w) v[w] = seq_mul2<T>(seq_mul2<T>(v[w], 0x7B807B80u), f2);
           }
           // 16 elements: units 2 ch and 2 ch + 1 of the row
 #pragma unroll
@@ -835,11 +886,10 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           ph ^= 1u;
         }
       };
-      const uint8_t *kb = static_cast<const uint8_t*>(K8), *vb = static_cast<const uint8_t*>(V8);
       for (int j = u.j0; j < j1; ++j) {
-        for (int k = u.j0; j == u.j0 && k < min(j1, u.j0 + C::AHEAD); ++k) load(kb, a.k_exp, ref[0], k);
-        if (j + C::AHEAD < j1) load(kb, a.k_exp, ref[0], j + C::AHEAD);
-        load(vb, a.v_exp, ref[1], j);
+        for (int k = u.j0; j == u.j0 && k < min(j1, u.j0 + C::AHEAD); ++k) load(0, k);
+        if (j + C::AHEAD < j1) load(0, j + C::AHEAD);
+        load(1, j);
       }
       __syncwarp();
       if (lane == 0) unit_done();

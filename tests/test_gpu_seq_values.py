@@ -1,0 +1,171 @@
+"""Attention over behaviour sequences on the GPU where the values are far apart, tiny, huge or zero:
+8-bit rows with powers of two of every size.
+
+Bounds, with u half a step of the 16-bit type and e_j = ES + 2^-23 d sum |q k_j| scale of each score (seq_util):
+  8-bit caches  key j's weight is off by P_j (u + 2 e_j), and every weight by the row sum's sum_j P_j e_j. Weights
+                are held in 16 bits together with their V row's power of two, relative to the row's largest such
+                product, so fp16's smallest step adds 2^-25 max_k(P_k 2^x_k) sum_j |v_j| (x the exponents, v
+                the e4m3 values).
+"""
+import numpy as np
+import pytest
+import torch
+
+import recsys_feature_interaction_b200 as wk
+from tests import seq_util as U
+from tests.test_gpu_seq import Cached, _attend, _check_attend, _ok, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_device):
+    from recsys_feature_interaction_b200 import build
+    build.build()
+    wk.lib()
+
+
+# ------------------------------------------------------------------ 8-bit rows of every size
+
+def _raw(c, b):
+    """(k, k exponents, v, v exponents) of sequence b, e4m3 values and powers in float64."""
+    pos = np.arange(c.kv[b])
+    page, row = c.host_table[b][pos // c.page], pos % c.page
+    out = []
+    for name in ("K", "V"):
+        out.append(U.f64(c.cache[name].float())[page, :, row])
+        out.append(np.ldexp(1.0, U.f64(c.cache[name + "_exp"]).astype(int)[page, :, row] - 127))
+    return out
+
+
+def _set(c, b, pos, name, values=None, exp=None):
+    """Rows `pos` of sequence b: e4m3 values (a number) and / or exponent bytes."""
+    pos = np.atleast_1d(pos)
+    page = torch.from_numpy(c.host_table[b][pos // c.page].astype(np.int64)).cuda()
+    row = torch.from_numpy(pos % c.page).cuda()
+    if values is not None:
+        x = torch.as_tensor(values, dtype=torch.float32).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+        c.cache[name].view(torch.uint8)[page, :, row] = x
+    if exp is not None:
+        c.cache[name + "_exp"][page, :, row] = torch.as_tensor(exp, dtype=torch.uint8).cuda()
+
+
+def _check8(c, q, n, O, causal):
+    at = 0
+    u, d = U.half_step(c.dt), c.d
+    least = torch.finfo(c.dt).smallest_normal * torch.finfo(c.dt).eps
+    for b, m in enumerate(n):
+        x = [U.expand(t, q.shape[1]) for t in _raw(c, b)[:1] + [_raw(c, b)[2]]]
+        kp, vp = (np.repeat(t, q.shape[1] // c.hk, axis=1) for t in (_raw(c, b)[1], _raw(c, b)[3]))
+        k, v = x[0] * kp[..., None], x[1] * vp[..., None]
+        qq = U.f64(q[at:at + m])
+        seen = np.array([max(0, c.kv[b] - m + i + 1) if causal else c.kv[b] for i in range(m)])
+        mask = (np.arange(c.kv[b])[None] < seen[:, None])[:, None]
+        S = np.where(mask, np.einsum("nhd,lhd->nhl", qq, k) / np.sqrt(d), -np.inf)
+        e = U.ES + 2.0 ** -23 * d * np.einsum("nhd,lhd->nhl", np.abs(qq), np.abs(k)) / np.sqrt(d)
+        top = S.max(axis=2, keepdims=True)
+        P = np.where(mask, np.exp(S - np.where(np.isfinite(top), top, 0.0)), 0.0)
+        P /= np.maximum(P.sum(axis=2, keepdims=True), 1e-300)
+        O_ref = np.einsum("nhl,lhd->nhd", P, v)
+        A = np.einsum("nhl,lhd->nhd", P, np.abs(v))
+        bound = np.einsum("nhl,lhd->nhd", P * (u + 2 * e), np.abs(v)) + 2 * (P * e).sum(axis=2, keepdims=True) * A
+        largest = (P * vp.T[None]).max(axis=2, keepdims=True)
+        bound += 2.0 ** -25 * largest * np.einsum("nhl,lhd->nhd", np.broadcast_to(mask, P.shape).astype(float),
+                                                  np.abs(x[1]))
+        U.check("O of sequence %d" % b, U.f64(O[at:at + m]), O_ref, 1.05 * bound + u * np.abs(O_ref) + least)
+        at += m
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [1, 3, 70])
+@pytest.mark.parametrize("d", [32, 128, 160])
+def test_keys_of_zeros(d, n, causal, dt):
+    """A history of zero rows (written with exponent 0): the output is the mean of V."""
+    gen = torch.Generator().manual_seed(1)
+    c = Cached([300, 77], 2, d, dt, 16, 8)
+    for b in range(2):
+        _set(c, b, np.arange(c.kv[b]), "K", 0.0, 0)
+    q = _rand(gen, c.dt, 2 * n, 4, d)
+    O, L = _attend(c, q, U.offsets([n, n]), n, causal)
+    _ok()
+    _check_attend(c, q, [n, n], O, L, causal)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n", [3, 40])
+def test_a_tail_of_zero_keys_in_a_cut_sequence(n, causal, dt):
+    """The last blocks' share of a long history holds nothing but zero rows, and ends inside a block of keys."""
+    gen = torch.Generator().manual_seed(2)
+    c = Cached([40017], 1, 64, dt, 128, 8)
+    _set(c, 0, np.arange(30000, 40017), "K", 0.0, 0)
+    q = _rand(gen, c.dt, n, 2, 64, std=0.2)
+    O, L = _attend(c, q, U.offsets([n]), n, causal)
+    _ok()
+    _check_attend(c, q, [n], O, L, causal)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [70])
+@pytest.mark.parametrize("gap", [25, 40, 90])
+def test_a_large_value_row_that_the_mask_hides(gap, n, dt):
+    """The newest token's V row is 2^gap above all others: only the last row sees it, the others' results are those
+    of the small rows. Its key's score is far below, so the last row's are theirs too."""
+    gen = torch.Generator().manual_seed(3)
+    c = Cached([200, 150], 1, 64, dt, 16, 8)
+    c.cache["V_exp"][:] = 118
+    for b in range(2):
+        _set(c, b, c.kv[b] - 1, "V", exp=118 + gap)
+        _set(c, b, c.kv[b] - 1, "K", -1.0, 127 + 9)  # about -700
+    q = _rand(gen, c.dt, 2 * n, 2, 64, std=0.2).abs() + 0.01
+    O, _ = _attend(c, q, U.offsets([n, n]), n, True)
+    _ok()
+    _check8(c, q, [n, n], O, True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [70])
+@pytest.mark.parametrize("place", [0, 64, 199])
+def test_a_large_value_row_with_next_to_no_weight(place, n, dt):
+    """Key `place` has a V row 2^30 above the others' and a score that leaves it a weight of about 2^-46."""
+    gen = torch.Generator().manual_seed(4)
+    c = Cached([200], 2, 128, dt, 32, 8)
+    c.cache["V_exp"][:] = 119
+    _set(c, 0, np.arange(200), "K", exp=112)
+    _set(c, 0, place, "V", exp=149)
+    _set(c, 0, place, "K", -2.0, 127)
+    q = torch.full((n, 4, 128), 1.4140625, dtype=c.dt, device="cuda")  # s = -32 for that key
+    O, _ = _attend(c, q, U.offsets([n]), n, False)
+    _ok()
+    _check8(c, q, [n], O, False)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 70])
+def test_large_keys_beside_small_ones(n, dt):
+    """Keys with exponents 60 above the others' and scores far below: the small ones share the weight by their scores."""
+    gen = torch.Generator().manual_seed(5)
+    c = Cached([300, 100], 1, 64, dt, 16, 8)
+    c.cache["K_exp"][:] = 122
+    for b in range(2):
+        _set(c, b, np.arange(7, c.kv[b], 50), "K", -1.0, 182)
+    q = _rand(gen, c.dt, 2 * n, 2, 64, std=0.1).abs() + 0.01
+    O, _ = _attend(c, q, U.offsets([n, n]), n, True)
+    _ok()
+    _check8(c, q, [n, n], O, True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n,kv,d,page", [([1, 1], [900, 31], 128, 64), ([4, 2], [100, 3000], 64, 16),
+                                         ([80, 33], [700, 33], 160, 32), ([200], [5000], 32, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_value_rows_of_every_size(causal, n, kv, d, page, dt):
+    """V's exponents drawn from 60 powers of two below 1, scores that differ."""
+    gen = torch.Generator().manual_seed(6)
+    c = Cached(kv, 2, d, dt, page, 8)
+    c.cache["V_exp"][:] = torch.randint(60, 120, c.cache["V_exp"].shape, generator=gen).to(torch.uint8).cuda()
+    q = _rand(gen, c.dt, sum(n), 6, d, std=1.0)
+    O, _ = _attend(c, q, U.offsets(n), max(n), causal)
+    _ok()
+    _check8(c, q, n, O, causal)
