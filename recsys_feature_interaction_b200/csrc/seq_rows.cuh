@@ -13,9 +13,11 @@
 // statistics are kept per warp and joined over the block's warps, and over blocks, at the end.
 //
 // 8-bit rows are converted to fp16, whatever the type of Q and O: e4m3 values are exact in it, and
-// one instruction converts two. The rows' powers of two stay apart: K's joins the fp32 score, V's
-// is multiplied onto the converted pair, relative to a reference that is raised (and O rescaled) when
-// a row is more than 2^7 above it, so that every row down to 2^-15 of the largest enters exactly.
+// one instruction converts two. The rows' powers of two stay apart: K's joins the fp32 score s, V's
+// the exponent of the weight, P = 2^(s + x - w), with w the running maximum of s + x over the keys that
+// the row sees, beside the row sum of 2^(s - m). So what a row gives does not depend on the size of
+// rows that have no weight. (Multiplied onto the converted values, relative to the largest row met, it
+// lost those 2^25 below it, and took two more instructions a pair against one exponential a weight.)
 // bf16 queries are scaled by a power of two of their own row, so that they are exact in fp16 down to
 // 2^-39 of the row's largest. (Shifting e4m3's bits into bf16's fields took four instructions a pair
 // and made the kernel wait for the ALU: 86 us at 64 sequences of up to 15,000 keys.)
@@ -73,11 +75,6 @@ __device__ __forceinline__ uint32_t seq_e4m3_f16(uint16_t w) {
 }
 __device__ __forceinline__ uint16_t seq_lo16(uint32_t w) { return static_cast<uint16_t>(w); }
 __device__ __forceinline__ uint16_t seq_hi16(uint32_t w) { return static_cast<uint16_t>(w >> 16); }
-
-// 2^dx in fp16 (dx <= 15), bits; 0 below its range.
-__device__ __forceinline__ uint32_t seq_pow_f16(int dx) {
-  return dx >= -14 ? static_cast<uint32_t>(dx + 15) << 10 : (dx >= -24 ? 1u << (dx + 24) : 0u);
-}
 
 // 8x8 transpose of 16-bit elements across the warp.
 __device__ __forceinline__ uint32_t seq_movmatrix(uint32_t x) {
@@ -196,10 +193,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
     least = min(least, most);
     const int kend = min(most, u.j1 * C::KB);
     float m[NQ][2], l[NQ][2], acc[NQ][C::DT][4];
-    int vref = -1000;  // reference exponent of V; set by the first step
+    float wm[NQ][2];  // 8-bit: what weights and acc are relative to (else m)
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      m[q][0] = m[q][1] = -INFINITY;
+      m[q][0] = m[q][1] = wm[q][0] = wm[q][1] = -INFINITY;
       l[q][0] = l[q][1] = 0.f;
 #pragma unroll
       for (int t = 0; t < C::DT; ++t)
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
 
     uint32_t kr[C::KS / 8][C::KCH * C::KCB / 4];
     uint32_t vr[C::KS / 4][C::VL / 4];
-    uint32_t ke[C::KS / 8], ve[C::KS / 4];
+    uint32_t ke[C::KS / 8], ve[C::KS / 8];  // exponents of K rows, and of the V rows of the same keys
     // a step's keys in groups of 16, each within one page: the group's first row (of the tensor or the
     // cache), or -1 where there is nothing to load
     int64_t at[C::KS / 16];
@@ -239,12 +236,15 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
 #pragma unroll
       for (int i = 0; i < C::KS / 8; ++i) {
         const int r = 8 * (i & 1);
-        ke[i] = 0;
+        ke[i] = ve[i] = 0;
         if (at[i / 2] >= 0 && (all || k0 + 16 * (i / 2) + r + g < kend)) {
           const char* p = k_lane + (at[i / 2] + r) * k_row;
 #pragma unroll
           for (int x = 0; x < C::KCH; ++x) seq_ldg<C::KCB>(p + x * 4 * C::KCB, &kr[i][x * (C::KCB / 4)]);
-          if constexpr (C::Q8) ke[i] = __ldg(a.k_exp + at[i / 2] + r + g);
+          if constexpr (C::Q8) {
+            ke[i] = __ldg(a.k_exp + at[i / 2] + r + g);
+            ve[i] = __ldg(a.v_exp + at[i / 2] + r + g);
+          }
         } else {
 #pragma unroll
           for (int x = 0; x < C::KCH * C::KCB / 4; ++x) kr[i][x] = 0u;
@@ -256,12 +256,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
 #pragma unroll
       for (int i = 0; i < C::KS / 4; ++i) {
         const int r = (i & 1) + 8 * ((i >> 1) & 1);
-        ve[i] = 0;
         if (at[i / 4] >= 0 && (all || k0 + 16 * (i / 4) + r + 2 * c < kend)) {
           const char* p = v_lane + (at[i / 4] + r) * v_row;
 #pragma unroll
           for (int x = 0; x < C::VCH; ++x) seq_ldg<C::VCB>(p + x * 8 * C::VCB, &vr[i][x * (C::VCB / 4)]);
-          if constexpr (C::Q8) ve[i] = __ldg(a.v_exp + at[i / 4] + r + 2 * c);
         } else {
 #pragma unroll
           for (int x = 0; x < C::VL / 4; ++x) vr[i][x] = 0u;
@@ -307,26 +305,34 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
 #pragma unroll
           for (int q = 0; q < NQ; ++q) mma_16816<CT>(s[q][t], a0, a1, a2, a3, qf[q][ks][0], qf[q][ks][1]);
         }
-      // factors of the scores: the scale, and the rows' exponents
-      float kf[C::KS / 8];
+      // factors of the scores: the scale, and K's powers of two; V's exponents
+      float kf[C::KS / 8], vx[C::KS / 8];
 #pragma unroll
       for (int t = 0; t < C::KS / 8; ++t) {
         kf[t] = scale_log2;
-        if constexpr (C::Q8) kf[t] *= seq_pow(ke[t]);
+        vx[t] = 0.f;
+        if constexpr (C::Q8) {
+          kf[t] *= seq_pow(ke[t]);
+          vx[t] = ve[t] == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(static_cast<int>(ve[t]) - 127);
+        }
       }
       const bool all1 = k1 + C::KS <= kend;
       if (all1) load_k(k1, true);
       else if (k1 < kend) load_k(k1, false);
-      // scores, and each thread's own maxima of its two columns
+      // scores, the exponents of the weights, and each thread's own maxima of its two columns
       bool up = false;
-      float mx[NQ][2];
+      float mx[NQ][2], wx[NQ][2];
+      float y[NQ][C::KS / 16][4];
       if (k0 + C::KS <= least) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int t = 0; t < C::KS / 16; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[q][t][e] *= kf[2 * t + (e >> 1)] * qpow[q][e & 1];
+            for (int e = 0; e < 4; ++e) {
+              s[q][t][e] *= kf[2 * t + (e >> 1)] * qpow[q][e & 1];
+              if constexpr (C::Q8) y[q][t][e] = s[q][t][e] + vx[2 * t + (e >> 1)];
+            }
       } else {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
@@ -335,48 +341,44 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int k = k0 + 16 * t + 8 * (e >> 1) + g;
-              s[q][t][e] = k < seen[q][e & 1] ? s[q][t][e] * (kf[2 * t + (e >> 1)] * qpow[q][e & 1]) : -INFINITY;
+              const bool sees = k < seen[q][e & 1];
+              s[q][t][e] = sees ? s[q][t][e] * (kf[2 * t + (e >> 1)] * qpow[q][e & 1]) : -INFINITY;
+              if constexpr (C::Q8) y[q][t][e] = sees ? s[q][t][e] + vx[2 * t + (e >> 1)] : -INFINITY;
             }
       }
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[q][e] = -INFINITY;
+          mx[q][e] = wx[q][e] = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < C::KS / 16; ++t) mx[q][e] = fmaxf(mx[q][e], fmaxf(s[q][t][e], s[q][t][e + 2]));
-          up |= mx[q][e] > m[q][e] + 8.f;
-        }
-      int top = -1000;
-      if constexpr (C::Q8) {
-#pragma unroll
-        for (int t = 0; t < C::KS / 4; ++t) top = max(top, ve[t] == 255 ? -1000 : static_cast<int>(ve[t]));
-        up |= top > vref + 7;
-      }
-      // The running maximum (and V's reference) moves only when a score is more than 2^8 above it (a
-      // row's exponent more than 2^7): one vote, and a reduction over the lanes only then.
-      if (__any_sync(0xffffffffu, up)) {
-        float vf = 1.f;
-        if constexpr (C::Q8) {
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          if (top > vref + 7) {  // uniform over the warp
-            vf = vref == -1000 ? 0.f : seq_ex2(static_cast<float>(vref - top));
-            vref = top;
+          for (int t = 0; t < C::KS / 16; ++t) {
+            mx[q][e] = fmaxf(mx[q][e], fmaxf(s[q][t][e], s[q][t][e + 2]));
+            if constexpr (C::Q8) wx[q][e] = fmaxf(wx[q][e], fmaxf(y[q][t][e], y[q][t][e + 2]));
           }
+          up |= mx[q][e] > m[q][e] + 8.f;
+          if constexpr (C::Q8) up |= wx[q][e] > wm[q][e] + 8.f;
         }
+      // The running maxima move only when a value is more than 2^8 above one: one vote, and a reduction
+      // over the lanes only then.
+      if (__any_sync(0xffffffffu, up)) {
+        // the higher of `high` and the lanes' x in `high`; returns 2^(high before - after)
+        auto raise = [&](float& high, float x) -> float {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+          const float now = fmaxf(high, x);
+          const float f = high == -INFINITY ? 0.f : seq_ex2(high - now);
+          high = now;
+          return f;
+        };
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float fac[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx[q][e] = fmaxf(mx[q][e], __shfl_xor_sync(0xffffffffu, mx[q][e], o));
-            const float mn = fmaxf(m[q][e], mx[q][e]);
-            fac[e] = m[q][e] == -INFINITY ? 0.f : seq_ex2(m[q][e] - mn);
-            m[q][e] = mn;
+            fac[e] = raise(m[q][e], mx[q][e]);
             l[q][e] *= fac[e];
-            fac[e] *= vf;
+            if constexpr (C::Q8) fac[e] = raise(wm[q][e], wx[q][e]);
           }
 #pragma unroll
           for (int t = 0; t < C::DT; ++t) {
@@ -387,11 +389,12 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
           }
         }
       }
-      // softmax weights
+      // row sums and weights
       uint32_t pb[NQ][C::KS / 16][2];
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         const float mz[2] = {m[q][0] == -INFINITY ? 0.f : m[q][0], m[q][1] == -INFINITY ? 0.f : m[q][1]};
+        const float wz[2] = {wm[q][0] == -INFINITY ? 0.f : wm[q][0], wm[q][1] == -INFINITY ? 0.f : wm[q][1]};
 #pragma unroll
         for (int t = 0; t < C::KS / 16; ++t) {
           float p[4];
@@ -399,20 +402,10 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
           for (int e = 0; e < 4; ++e) {
             p[e] = seq_ex2(s[q][t][e] - mz[e & 1]);
             l[q][e & 1] += p[e];
+            if constexpr (C::Q8) p[e] = seq_ex2(y[q][t][e] - wz[e & 1]);
           }
           pb[q][t][0] = seq_movmatrix(Half16<CT>::pack2(p[0], p[1]));
           pb[q][t][1] = seq_movmatrix(Half16<CT>::pack2(p[2], p[3]));
-        }
-      }
-      uint32_t vfac[C::KS / 8];
-      if constexpr (C::Q8) {
-#pragma unroll
-        for (int t = 0; t < C::KS / 8; ++t) {
-          uint32_t f[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            f[e] = ve[2 * t + e] == 255 ? 0x7E00u : seq_pow_f16(static_cast<int>(ve[2 * t + e]) - vref);
-          vfac[t] = f[0] | (f[1] << 16);
         }
       }
       // O^T += V^T P^T
@@ -427,8 +420,8 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
               const int e = 2 * dt, wd = e / 4;  // elements e, e + 1: bytes of word wd
               // byte e of both keys, then byte e + 1 of both
               const uint32_t w = __byte_perm(vr[4 * t + 2 * h][wd], vr[4 * t + 2 * h + 1][wd], (e % 4) ? 0x7362 : 0x5140);
-              f[2 * h] = seq_mul2<__half>(seq_e4m3_f16(seq_lo16(w)), vfac[2 * t + h]);
-              f[2 * h + 1] = seq_mul2<__half>(seq_e4m3_f16(seq_hi16(w)), vfac[2 * t + h]);
+              f[2 * h] = seq_e4m3_f16(seq_lo16(w));
+              f[2 * h + 1] = seq_e4m3_f16(seq_hi16(w));
             } else {
               const uint32_t x = vr[4 * t + 2 * h][dt], y = vr[4 * t + 2 * h + 1][dt];
               f[2 * h] = __byte_perm(x, y, 0x5410);
@@ -443,13 +436,15 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
     }
 
     // the row sums over the lanes of a column, then the block's warps together
-    const float vscale = C::Q8 ? (vref == -1000 ? 0.f : seq_pow(vref)) : 1.f;
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], o);
+        // the square root of 2^(w - m), which fp32 holds whatever V's exponents are
+        float between = 1.f;
+        if constexpr (C::Q8) between = wm[q][e] == -INFINITY ? 0.f : seq_ex2(0.5f * (wm[q][e] - m[q][e]));
         if (g == 0) {
           sm_m[warp][8 * q + 2 * c + e] = m[q][e];
           sm_l[warp][8 * q + 2 * c + e] = l[q][e];
@@ -458,7 +453,7 @@ __global__ void __launch_bounds__(SEQ_ROWS_THREADS, seq_rows_occupancy(D, NQ, SR
         for (int t = 0; t < C::DT; ++t)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
-            sm_o[warp][8 * q + 2 * c + e][C::vd(t, half, g)] = acc[q][t][2 * half + e] * vscale;
+            sm_o[warp][8 * q + 2 * c + e][C::vd(t, half, g)] = acc[q][t][2 * half + e] * between * between;
       }
     __syncthreads();
     const bool whole = u.j0 == 0 && u.j1 == u.nb;

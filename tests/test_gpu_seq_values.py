@@ -107,7 +107,7 @@ def test_a_tail_of_zero_keys_in_a_cut_sequence(n, causal, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
-@pytest.mark.parametrize("n", [70])
+@pytest.mark.parametrize("n", [2, 70])
 @pytest.mark.parametrize("gap", [25, 40, 90])
 def test_a_large_value_row_that_the_mask_hides(gap, n, dt):
     """The newest token's V row is 2^gap above all others: only the last row sees it, the others' results are those
@@ -125,7 +125,7 @@ def test_a_large_value_row_that_the_mask_hides(gap, n, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
-@pytest.mark.parametrize("n", [70])
+@pytest.mark.parametrize("n", [1, 70])
 @pytest.mark.parametrize("place", [0, 64, 199])
 def test_a_large_value_row_with_next_to_no_weight(place, n, dt):
     """Key `place` has a V row 2^30 above the others' and a score that leaves it a weight of about 2^-46."""
