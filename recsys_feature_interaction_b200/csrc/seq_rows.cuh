@@ -51,22 +51,6 @@ __device__ __forceinline__ void seq_ldg(const void* p, uint32_t* r) {
   }
 }
 
-// x * y on a pair of 16-bit values.
-template <typename T>
-__device__ __forceinline__ uint32_t seq_mul2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  if constexpr (Half16<T>::kBF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
-// Two e4m3 values in bytes 1 and 3 as two values of T, times 2^-8 (fp16) or 2^-120 (bf16).
-template <typename T>
-__device__ __forceinline__ uint32_t seq_raw2(uint32_t w) {
-  return Half16<T>::kBF16 ? ((w & 0x80008000u) | ((w >> 4) & 0x07F007F0u))
-                          : ((w & 0x80008000u) | ((w >> 1) & 0x3F803F80u));
-}
-
 // Two e4m3 values as two fp16 values.
 __device__ __forceinline__ uint32_t seq_e4m3_f16(uint16_t w) {
   uint32_t r;

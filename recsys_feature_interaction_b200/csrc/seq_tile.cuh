@@ -19,7 +19,7 @@
 // the row sees, beside the row sum of 2^(S - m). So a row's share does not depend on what other rows
 // hold, seen or not. (With rows relative to the largest of the piece, those 2^22 below it lost bits.)
 // The second exponential costs less than the simpler conversion saves: chunks of 200 .. 512 tokens over
-// up to 4096 keys (d = 128, 8 heads on 2) take 143 us in fp16, 152 in bf16.
+// up to 4096 keys (d = 128, 8 heads on 2) take 143 us in fp16, 147 in bf16.
 //
 // Rows behind a sequence's last key belong to someone else: their scores are replaced by a select,
 // and their V rows, whose weights are 0, are overwritten with zeros in the tile before P V, because
@@ -104,6 +104,12 @@ __device__ __forceinline__ void seq_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(idesc), "r"(add), "n"(HI)
       : "memory");
+}
+
+// Two e4m3 values times a power of two as a pair of bf16, which holds every such product; NaN stays NaN.
+__device__ __forceinline__ uint32_t seq_e4m3_bf16(uint16_t w, float f) {
+  const uint32_t h = seq_e4m3_f16(w);
+  return pack_bf16x2(Half16<__half>::lo(h) * f, Half16<__half>::hi(h) * f);
 }
 
 // max(a, b, c) and max(a, b) that give NaN if an operand is NaN.
@@ -860,15 +866,12 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             }
           } else {
             const float f = seq_pow(e[i]);
-            const uint32_t f2 = Half16<T>::pack2(f, f);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const uint32_t b = reinterpret_cast<const uint32_t*>(&x[i])[w];
-              v[2 * w] = seq_raw2<T>(__byte_perm(b, 0u, 0x1404));      // bytes 0, 1 at places 1, 3
-              v[2 * w + 1] = seq_raw2<T>(__byte_perm(b, 0u, 0x3424));  // bytes 2, 3
+              v[2 * w] = seq_e4m3_bf16(seq_lo16(b), f);
+              v[2 * w + 1] = seq_e4m3_bf16(seq_hi16(b), f);
             }
-#pragma unroll
-            for (int w = 0; w < 8; ++w) v[w] = seq_mul2<T>(seq_mul2<T>(v[w], 0x7B807B80u), f2);
           }
           // 16 elements: units 2 ch and 2 ch + 1 of the row
 #pragma unroll

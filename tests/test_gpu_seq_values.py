@@ -1,5 +1,5 @@
-"""Attention over behaviour sequences on the GPU where the values are far apart, tiny, huge or zero:
-8-bit rows with powers of two of every size.
+"""Attention over behaviour sequences on the GPU where the values are far apart, tiny, huge, zero or not finite:
+8-bit rows with powers of two of every size, NaN bytes, single infinite scores.
 
 Bounds, with u half a step of the 16-bit type and e_j = ES + 2^-23 d sum |q k_j| scale of each score (seq_util):
   8-bit caches  key j's weight is off by P_j (u + 2 e_j), and every weight by the row sum's sum_j P_j e_j. Weights
@@ -13,7 +13,7 @@ import torch
 
 import recsys_feature_interaction_b200 as wk
 from tests import seq_util as U
-from tests.test_gpu_seq import Cached, _attend, _check_attend, _ok, _rand
+from tests.test_gpu_seq import Cached, Jagged, _attend, _check_attend, _ok, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,49 @@ def test_value_rows_of_every_size(causal, n, kv, d, page, dt):
     O, _ = _attend(c, q, U.offsets(n), max(n), causal)
     _ok()
     _check8(c, q, n, O, causal)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("byte", [0x7F, 0xFF])
+def test_a_nan_byte_in_an_ordinary_row(byte, n, dt):
+    """e4m3's NaN in a row with an ordinary exponent: in V one column of the output, in K every row that sees it."""
+    gen = torch.Generator().manual_seed(7)
+    c = Cached([200, 90], 1, 64, dt, 16, 8)
+    q = _rand(gen, c.dt, n + 1, 2, 64, std=0.2)
+    off = U.offsets([n, 1])
+    good, _ = _attend(c, q, off, n, False)
+    _ok()
+    page = int(c.host_table[0][3])
+    v = c.cache["V"].view(torch.uint8)
+    keep = v[page, 0, 4, 37].item()
+    v[page, 0, 4, 37] = byte
+    O, _ = _attend(c, q, off, n, False)
+    _ok()
+    assert torch.isnan(O[:n, :, 37].float()).all()
+    rest = [i for i in range(64) if i != 37]
+    assert torch.equal(O[:, :, rest], good[:, :, rest]) and torch.equal(O[n:], good[n:])
+    v[page, 0, 4, 37] = keep
+    c.cache["K"].view(torch.uint8)[page, 0, 4, 11] = byte
+    O, _ = _attend(c, q, off, n, False)
+    _ok()
+    assert torch.isnan(O[:n].float()).all() and torch.equal(O[n:], good[n:])
+
+
+# ------------------------------------------------------------------------ infinite scores
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_one_infinite_score(n, dt):
+    """A single score of +inf makes the softmax NaN, whichever key it belongs to."""
+    j = Jagged([n, n], [200, 200], 1, 1, 64, dt, behind=0)
+    j.q[:, :, 9] = j.q[:, :, 9].abs() + 0.1
+    clean, _ = j.forward()
+    for key in [*range(16), 62, 63, 126, 127, 128, 199]:
+        keep = j.k[key, 0, 9].item()
+        j.k[key, 0, 9] = float("inf")
+        O, _ = j.forward()
+        _ok()
+        assert torch.isnan(O[:n].float()).all(), key
+        assert torch.equal(O[n:], clean[n:]), key
+        j.k[key, 0, 9] = keep
