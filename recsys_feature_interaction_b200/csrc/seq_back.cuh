@@ -73,6 +73,16 @@ struct SbCfg {
   static_assert((2 * SBUF + 2 * STAGES + 7 + 2 * NU) * 8 + 8 <= BARB, "barriers");
 };
 
+// What a weight of 1 is held as in DKV's operand P. A key of a long history has weights of 2^-14 and
+// far below, where fp16 has few bits left or none, and dV adds up ordinary numbers of them. Times 2^12
+// weights from 2^-26 on keep all bits, and 2^4 are left for scores so large that fp32's rounding of
+// them (the difference of score and lse) lifts a weight above 1. bf16 has the range of fp32.
+template <typename T>
+struct SbP {
+  static constexpr int LOG2 = Half16<T>::kBF16 ? 0 : 12;
+  static constexpr float ONE = static_cast<float>(1 << LOG2);
+};
+
 template <int D, typename T, bool DKV>
 __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     seq_back_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmA2,
@@ -350,6 +360,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const int bar_id = 1 + q;
     const float scale_log2 = a.scale * 1.4426950408889634f;
+    constexpr float UP = SbP<T>::LOG2;
     uint8_t* stage = reinterpret_cast<uint8_t*>(red) + C::REDB + (warp - 4) * SEQ_STAGE_BYTES;
     float* cols = red + (warp - 4) * 128;  // DKV: lse (base 2) [32] and delta [32] of this warp's columns, twice
     uint32_t g = 0, uc = 0;
@@ -452,8 +463,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
               float p[4], s[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                p[e] = whale_ex2(fmaf(__uint_as_float(t1[4 * c4 + e]), scale_log2, -lv[e]));
-                s[e] = p[e] * ((__uint_as_float(t2[4 * c4 + e]) - dv[e]) * a.scale);
+                p[e] = whale_ex2(fmaf(__uint_as_float(t1[4 * c4 + e]), scale_log2, UP - lv[e]));
+                s[e] = p[e] * ((__uint_as_float(t2[4 * c4 + e]) - dv[e]) * (a.scale * (1.f / SbP<T>::ONE)));
               }
               pp[2 * c4] = Half16<T>::pack2(p[0], p[1]);
               pp[2 * c4 + 1] = Half16<T>::pack2(p[2], p[3]);
@@ -521,14 +532,15 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::ACOL + cc * 32, o);
             tmem_ld_wait();
+            const float f = cc < D / 32 ? 1.f : 1.f / SbP<T>::ONE;
             if (whole) {
-              seq_store_rows<D, T>(stage, o, 1.f, cc < D / 32 ? G1 : G2, (cc % (D / 32)) * 32, out);
+              seq_store_rows<D, T>(stage, o, f, cc < D / 32 ? G1 : G2, (cc % (D / 32)) * 32, out);
             } else if (row_on && ok) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 *reinterpret_cast<float4*>(S::o(slot, row, cc * 32 + 4 * i)) =
-                    make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
             }
           }
         }

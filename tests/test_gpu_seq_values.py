@@ -1,11 +1,15 @@
 """Attention over behaviour sequences on the GPU where the values are far apart, tiny, huge, zero or not finite:
-8-bit rows with powers of two of every size, NaN bytes, single infinite scores.
+8-bit rows with powers of two of every size, NaN bytes, single infinite scores, fp16
+gradients.
 
 Bounds, with u half a step of the 16-bit type and e_j = ES + 2^-23 d sum |q k_j| scale of each score (seq_util):
   8-bit caches  key j's weight is off by P_j (u + 2 e_j), and every weight by the row sum's sum_j P_j e_j. Weights
                 are held in 16 bits together with their V row's power of two, relative to the row's largest such
                 product, so fp16's smallest step adds 2^-25 max_k(P_k 2^x_k) sum_j |v_j| (x the exponents, v
                 the e4m3 values).
+  fp16 grads    P (dP - delta) enters relative to a power of two at least 2^10 / (|dO| |V|), |dO| the norm of the
+                row (dQ) or the largest of the rows that share a key head (dK), |V| the largest of the sequence:
+                fp16's smallest step adds 2^-25 2^-10 |dO| |V|. P enters dV times 2^12: 2^-37.
 """
 import numpy as np
 import pytest
@@ -215,3 +219,63 @@ def test_one_infinite_score(n, dt):
         assert torch.isnan(O[:n].float()).all(), key
         assert torch.equal(O[n:], clean[n:]), key
         j.k[key, 0, 9] = keep
+
+
+# ------------------------------------------------------------------------ fp16 gradients
+
+def _grad_bounds(q, k, v, g, scale):
+    """{name: (reference, bound)} of one sequence, fp16 (see the head of this file)."""
+    n, hq, d = q.shape
+    L, hk, _ = k.shape
+    u, least = 2.0 ** -11 / 2, 2.0 ** -24
+    ke, ve = U.expand(k, hq), U.expand(v, hq)
+    S = np.einsum("nhd,lhd->nhl", q, ke) * scale
+    e = (U.ES + 2.0 ** -23 * d * np.einsum("nhd,lhd->nhl", np.abs(q), np.abs(ke)) * scale).max(axis=2, keepdims=True)
+    P = np.exp(S - S.max(axis=2, keepdims=True))
+    P /= P.sum(axis=2, keepdims=True)
+    O = np.einsum("nhl,lhd->nhd", P, ve)
+    eO = 1.05 * ((u + 2 * e) * np.einsum("nhl,lhd->nhd", P, np.abs(ve)) + 2.0 ** -25 * np.abs(ve).sum(axis=0)[None])
+    G, Gm = np.einsum("nhd,lhd->nhl", g, ve), np.einsum("nhd,lhd->nhl", np.abs(g), np.abs(ve))
+    delta = (g * O).sum(axis=2, keepdims=True)
+    e_delta = (np.abs(g) * (eO + u * np.abs(O) + least)).sum(axis=2, keepdims=True) \
+        + 2.0 ** -23 * d * (np.abs(g) * np.abs(O)).sum(axis=2, keepdims=True)
+    dS = P * (G - delta)
+    e_dS = (np.abs(dS) * (u + 2 * e) + P * (1 + 2 * e) * (e_delta + 2.0 ** -23 * d * Gm)) * 1.05
+    norm = np.sqrt((g ** 2).sum(axis=2, keepdims=True)) * np.sqrt((ve ** 2).sum(axis=2)).max(axis=0)[None, :, None]
+    share = np.repeat(norm.max(axis=0).reshape(hk, -1).max(axis=1), hq // hk)[None, :, None]
+
+    def fold(x):
+        return x.reshape(L, hk, hq // hk, d).sum(axis=2)
+
+    out = {}
+    dQ = np.einsum("nhl,lhd->nhd", dS, ke) * scale
+    out["dQ"] = (dQ, np.einsum("nhl,lhd->nhd", e_dS + 2.0 ** -35 * norm, np.abs(ke)) * scale + u * np.abs(dQ) + least)
+    dK = fold(np.einsum("nhl,nhd->lhd", dS, q)) * scale
+    out["dK"] = (dK, fold(np.einsum("nhl,nhd->lhd", e_dS + 2.0 ** -35 * share, np.abs(q))) * scale + u * np.abs(dK) + least)
+    dV = fold(np.einsum("nhl,nhd->lhd", P, g))
+    out["dV"] = (dV, fold(np.einsum("nhl,nhd->lhd", P * (u + 2 * e) * 1.05 + 2.0 ** -37, np.abs(g))) + u * np.abs(dV) + least)
+    return out
+
+
+def _check_grads(j, grads, scale, names=("dQ", "dK", "dV")):
+    qa = ka = 0
+    q, k, v, g = (U.f64(t) for t in (j.q, j.k, j.v, j.g))
+    for b, (n, kv) in enumerate(zip(j.n, j.kv)):
+        if n and kv:
+            want = _grad_bounds(q[qa:qa + n], k[ka:ka + kv], v[ka:ka + kv], g[qa:qa + n], scale)
+            for name, t, at, m in zip(("dQ", "dK", "dV"), grads, (qa, ka, ka), (n, kv, kv)):
+                if name in names:
+                    U.check("%s of sequence %d" % (name, b), U.f64(t[at:at + m]), *want[name])
+        qa, ka = qa + n, ka + kv
+
+
+def test_weights_below_halfs_normal_range_reach_dv():
+    """Keys with softmax weights of 2^-16 to 2^-22: their value gradients are ordinary numbers."""
+    j = Jagged([60], [4000], 1, 1, 64, "f16", behind=0)
+    j.q[:, :, 0], j.k[:, :, 0] = 1.0, -64.0  # all but the first 8 keys: 13 below
+    j.k[:8, :, 0] = 40.0
+    j.g *= 64.0
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    _check_grads(j, grads, 1 / 8, ("dV",))
