@@ -516,8 +516,10 @@ WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_wha
  * left out, the result is not valid, and wk_device_status returns WK_ERR_DEVICE.
  *
  * Arithmetic: 16-bit inputs and outputs; products accumulate in fp32; scores, softmax statistics
- * and lse are fp32; the softmax weights and the gradients of the scores are rounded to the 16-bit
- * type as tensor-core operands. Results do not depend on the order in which blocks run. */
+ * and lse are fp32 (lse off by up to 1e-4, the error of one exponential); the softmax weights and the
+ * gradients of the scores are rounded to the 16-bit type as tensor-core operands. fp16 gradients take
+ * a power of two out first, from the norms of dO and V, so that a loss of any size uses fp16's range
+ * from the top. Results do not depend on the order in which blocks run. */
 
 typedef struct {
   int32_t batch;               /* sequences, >= 0 */

@@ -73,6 +73,103 @@ struct SbCfg {
   static_assert((2 * SBUF + 2 * STAGES + 7 + 2 * NU) * 8 + 8 <= BARB, "barriers");
 };
 
+// How large a unit's dS can be, for fp16. |dP - delta| <= 2 |dO_i| max_j |V_j| (norms of rows), so dS
+// enters its product times the power of two that takes this bound to at most 2^12, and dQ and dK are
+// scaled back in fp32, with `scale` too: a loss of any size uses fp16's range from the top, with all
+// bits down to 2^-26 of the bound. (Times `scale` alone, with dO of 2^-10 over 2048 keys, dQ was off by
+// 2 %; with dO V^T beyond 65504 it was infinite.) The norms come from a pass over V and dO before the
+// two kernels: the largest of each chunk of 32 tokens, so that a unit reads few, and each dO row's own,
+// because the rows' losses differ. It makes a training step at the 2-layer shape 140 us in fp16, so 128;
+// bf16 does without.
+constexpr int SEQ_CHUNK = 32;
+struct SeqRange {
+  float* rows;  // [total_q, q_heads] squared norms of dO
+  float* g;     // [total_q / SEQ_CHUNK + batch, kv_heads] the largest of a chunk of a sequence's tokens
+  float* v;     // [total_kv / SEQ_CHUNK + batch, kv_heads] the same of V
+};
+
+// A sequence's chunks: those of sequences before it end below (begin / SEQ_CHUNK + b).
+__device__ __forceinline__ int64_t seq_chunk(int64_t begin, int64_t b, int c, int kv_heads, int h) {
+  return (begin / SEQ_CHUNK + b + c) * kv_heads + h;
+}
+
+// The largest over the chunks of `rows` rows, for the whole warp.
+__device__ __forceinline__ float seq_chunks_max(const float* chunks, int64_t begin, int64_t b, int rows, int kv_heads,
+                                                int h) {
+  float x = 0.f;
+  for (int c = threadIdx.x & 31; c < (rows + SEQ_CHUNK - 1) / SEQ_CHUNK; c += 32)
+    x = fmaxf(x, __ldg(chunks + seq_chunk(begin, b, c, kv_heads, h)));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// k with 2 sqrt(x) 2^k in (2^10, 2^12]; 0 where there is no such bound (zero, infinite, NaN).
+__device__ __forceinline__ int seq_range_log2(float x) {
+  const uint32_t e = __float_as_uint(x) >> 23;
+  if (e == 0 || e >= 255) return 0;
+  return 11 - ((static_cast<int>(e) - 127 + 2) >> 1);
+}
+__device__ __forceinline__ float seq_exp2i(int k) { return __uint_as_float(static_cast<uint32_t>(127 + k) << 23); }
+
+// The warps of blocks (b, V or dO, z) take the (chunk, key head) of sequence b in turn, four lanes to a
+// row and 16 rows' loads at a time; bound by the latency of offsets, rows and the reduction, one after
+// the other (33 MB of V at the 2-layer shape: 12.4 us of cold inputs; 14.3 with chunks of 128 and a block
+// each, 14.1 with two chunks to a warp and 32 rows at a time).
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+    seq_range_kernel(const T* __restrict__ V, const T* __restrict__ dO, SeqRange out, SeqArgs a) {
+  seq_wait_before();
+  const int lane = threadIdx.x & 31, group = a.q_heads / a.kv_heads;
+  const int64_t b = blockIdx.x;
+  const bool is_v = blockIdx.y == 0;
+  const SeqSpan span = is_v ? seq_keys<SEQ_JAGGED>(a, b) : seq_queries(a, b);
+  const int each = is_v ? 1 : group;  // rows of a token
+  const int tasks = (span.len + SEQ_CHUNK - 1) / SEQ_CHUNK * a.kv_heads;
+  for (int task = blockIdx.z * 8 + (threadIdx.x >> 5); task < tasks; task += gridDim.z * 8) {
+    const int c = task / a.kv_heads, h = task % a.kv_heads;
+    const int rows = min(SEQ_CHUNK, span.len - c * SEQ_CHUNK) * each;
+    float top = 0.f;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+      uint4 y[2][D / 32];
+      int64_t row[2];  // of dO
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = r0 + 8 * j + (lane >> 2);
+        const int64_t token = span.begin + c * SEQ_CHUNK + r / each;
+        row[j] = token * a.q_heads + h * group + r % each;
+        const uint4* p =
+            reinterpret_cast<const uint4*>(is_v ? V + token * a.v_stride + h * D : dO + row[j] * D) + (lane & 3);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          y[j][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) y[j][i] = __ldg(p + 4 * i);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w = reinterpret_cast<const uint32_t*>(&y[j][i])[k];
+            x = fmaf(Half16<T>::lo(w), Half16<T>::lo(w), x);
+            x = fmaf(Half16<T>::hi(w), Half16<T>::hi(w), x);
+          }
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if (!is_v && r0 + 8 * j + (lane >> 2) < rows && (lane & 3) == 0) out.rows[row[j]] = x;
+        top = fmaxf(top, x);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) (is_v ? out.v : out.g)[seq_chunk(span.begin, b, c, a.kv_heads, h)] = top;
+  }
+}
+
 // What a weight of 1 is held as in DKV's operand P. A key of a long history has weights of 2^-14 and
 // far below, where fp16 has few bits left or none, and dV adds up ordinary numbers of them. Times 2^12
 // weights from 2^-26 on keep all bits, and 2^4 are left for scores so large that fp32's rounding of
@@ -88,8 +185,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     seq_back_kernel(const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmA2,
                     const __grid_constant__ CUtensorMap tmY1, const __grid_constant__ CUtensorMap tmY2,
                     const T* __restrict__ O, const T* __restrict__ dO, const float* __restrict__ lse,
-                    float* __restrict__ delta, T* __restrict__ G1, T* __restrict__ G2, float* __restrict__ ws,
-                    SeqArgs a, int64_t pieces) {
+                    float* __restrict__ delta, SeqRange range, T* __restrict__ G1, T* __restrict__ G2,
+                    float* __restrict__ ws, SeqArgs a, int64_t pieces) {
   using C = SbCfg<D, DKV>;
   using P = SeqPlanBack<DKV>;
   using S = SeqSlots<128, C::NACC * D>;
@@ -365,6 +462,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     float* cols = red + (warp - 4) * 128;  // DKV: lse (base 2) [32] and delta [32] of this warp's columns, twice
     uint32_t g = 0, uc = 0;
     bool ok = true;
+    int high_at = -1;  // fp16: the (sequence, key head) whose largest norms `high` holds
+    float high = 0.f;
     SeqUnit u;
     for (;;) {
       const bool got = ok && unit_take(u);
@@ -380,7 +479,20 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
                            : DKV   ? (u.kv_begin + r) * a.kv_heads + u.h
                                    : (u.q_begin + r / group) * a.q_heads + u.h * group + r % group;
       if (u.j0 < j1) {
+        // dS goes into its product times ds_in, the sums come out times ds_out
+        float ds_in = a.scale, ds_out = 1.f;
         float lse2 = 0.f, dl = 0.f;
+        if constexpr (!Half16<T>::kBF16) {
+          const int at = u.b * a.kv_heads + u.h;
+          if (at != high_at) {
+            high_at = at;
+            high = seq_chunks_max(range.v, u.kv_begin, u.b, u.len, a.kv_heads, u.h);
+            if constexpr (DKV) high *= seq_chunks_max(range.g, u.q_begin, u.b, u.n, a.kv_heads, u.h);
+          }
+          const int k = seq_range_log2(DKV ? high : high * (row_on ? __ldg(range.rows + orow) : 0.f));
+          ds_in = seq_exp2i(k - (DKV ? SbP<T>::LOG2 : 0));
+          ds_out = a.scale * seq_exp2i(-k);
+        }
         const bool one = !DKV && u.nb == 1;  // every key in one block
         if constexpr (!DKV) {
           if (row_on) lse2 = __ldg(lse + orow) * 1.4426950408889634f;
@@ -464,7 +576,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 p[e] = whale_ex2(fmaf(__uint_as_float(t1[4 * c4 + e]), scale_log2, UP - lv[e]));
-                s[e] = p[e] * ((__uint_as_float(t2[4 * c4 + e]) - dv[e]) * (a.scale * (1.f / SbP<T>::ONE)));
+                s[e] = p[e] * ((__uint_as_float(t2[4 * c4 + e]) - dv[e]) * ds_in);
               }
               pp[2 * c4] = Half16<T>::pack2(p[0], p[1]);
               pp[2 * c4 + 1] = Half16<T>::pack2(p[2], p[3]);
@@ -509,8 +621,8 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
               uint32_t ds[16];
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float s0 = __uint_as_float(t1[2 * c]) * ((__uint_as_float(t2[2 * c]) - dl) * a.scale);
-                const float s1 = __uint_as_float(t1[2 * c + 1]) * ((__uint_as_float(t2[2 * c + 1]) - dl) * a.scale);
+                const float s0 = __uint_as_float(t1[2 * c]) * ((__uint_as_float(t2[2 * c]) - dl) * ds_in);
+                const float s1 = __uint_as_float(t1[2 * c + 1]) * ((__uint_as_float(t2[2 * c + 1]) - dl) * ds_in);
                 ds[c] = Half16<T>::pack2(s0, s1);
               }
               if (warp_on) whale_tmem_st_cols<16>(tb + at, ds);
@@ -532,7 +644,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
             uint32_t o[32];
             tmem_ld32(tmem + lane_base + C::ACOL + cc * 32, o);
             tmem_ld_wait();
-            const float f = cc < D / 32 ? 1.f : 1.f / SbP<T>::ONE;
+            const float f = cc < D / 32 ? ds_out : 1.f / SbP<T>::ONE;
             if (whole) {
               seq_store_rows<D, T>(stage, o, f, cc < D / 32 ? G1 : G2, (cc % (D / 32)) * 32, out);
             } else if (row_on && ok) {

@@ -282,14 +282,20 @@ struct RunForward {
   }
 };
 
-// ---- the backward (seq_back.cuh): delta [total_q, q_heads], then the partial results, which the
-// two kernels use one after the other
-int64_t delta_bytes(const SeqArgs& a) { return (a.total_q * a.q_heads * 4 + 255) / 256 * 256; }
+// ---- the backward (seq_back.cuh): delta [total_q, q_heads], with fp16 the norms of dO and V, then the
+// partial results, which the two kernels use one after the other
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+int64_t delta_bytes(const SeqArgs& a) { return up256(a.total_q * a.q_heads * 4); }
+// bytes of the chunks of a jagged tensor (SeqRange)
+int64_t chunk_bytes(const SeqArgs& a, int64_t total) { return up256((total / SEQ_CHUNK + a.batch) * a.kv_heads * 4); }
+int64_t range_bytes(const SeqArgs& a, wk_dtype t) {
+  return t == WK_F16 ? delta_bytes(a) + chunk_bytes(a, a.total_q) + chunk_bytes(a, a.total_kv) : 0;
+}
 int dkv_block(const SeqArgs& a) { return (a.q_heads / a.kv_heads) * (64 / (a.q_heads / a.kv_heads)); }
 bool dq_cut(const SeqArgs& a) { return a.max_kv > 2 * kUncut * 64; }
 bool dkv_cut(const SeqArgs& a) { return packed_rows(a) > 2 * kUncut * dkv_block(a); }
-int64_t backward_ws(const SeqArgs& a, int d) {
-  return delta_bytes(a) + (dkv_cut(a) ? slot_bytes(128, 2 * d, kSMs) : dq_cut(a) ? slot_bytes(128, d, kSMs) : 0);
+int64_t backward_ws(const SeqArgs& a, int d, wk_dtype t) {
+  return delta_bytes(a) + range_bytes(a, t) + (dkv_cut(a) ? slot_bytes(128, 2 * d, kSMs) : dq_cut(a) ? slot_bytes(128, d, kSMs) : 0);
 }
 
 struct RunBackward {
@@ -302,7 +308,7 @@ struct RunBackward {
   cudaStream_t st;
 
   template <int D, typename T, bool DKV>
-  wk_status one(const CUtensorMap (&m)[4], float* delta, float* slots, void* G1, void* G2) const {
+  wk_status one(const CUtensorMap (&m)[4], float* delta, const SeqRange& range, float* slots, void* G1, void* G2) const {
     using C = SbCfg<D, DKV>;
     SeqArgs x = a;
     const int group = a.q_heads / a.kv_heads;
@@ -313,7 +319,7 @@ struct RunBackward {
     wk_status s = smem_attr(dv, reinterpret_cast<const void*>(fn), C::SMEM);
     if (s != WK_OK) return s;
     s = launch(fn, kSMs, C::THREADS, C::SMEM, st, m[0], m[1], m[2], m[3], static_cast<const T*>(O),
-               static_cast<const T*>(dO), lse, delta, static_cast<T*>(G1), static_cast<T*>(G2),
+               static_cast<const T*>(dO), lse, delta, range, static_cast<T*>(G1), static_cast<T*>(G2),
                x.uncut ? nullptr : slots, x, int64_t{kSMs});
     if (s != WK_OK || x.uncut) return s;
     constexpr int CR = 16 / C::NACC;
@@ -340,13 +346,29 @@ struct RunBackward {
         !rows(&k[2], Q, a.q_stride, 64) || !rows(&k[3], dO, od, 64))
       return WK_ERR_UNSUPPORTED;
     float* delta = static_cast<float*>(workspace);
-    float* slots = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes(a));
+    uint8_t* rest = static_cast<uint8_t*>(workspace) + delta_bytes(a);
+    SeqRange range{};
+    if constexpr (!Half16<T>::kBF16) {
+      range.rows = reinterpret_cast<float*>(rest);
+      range.g = reinterpret_cast<float*>(rest + delta_bytes(a));
+      range.v = reinterpret_cast<float*>(rest + delta_bytes(a) + chunk_bytes(a, a.total_q));
+      rest += range_bytes(a, WK_F16);
+      if (a.total_q > 0 && a.total_kv > 0) {
+        // a warp to a chunk, as long as that is not many times the blocks that the SMs hold
+        const int64_t chunks = (static_cast<int64_t>(std::max(a.max_q, a.max_kv)) + SEQ_CHUNK - 1) / SEQ_CHUNK * a.kv_heads;
+        const unsigned z = static_cast<unsigned>(std::clamp<int64_t>((chunks + 7) / 8, 1, std::max(1, 16 * kSMs / a.batch)));
+        const wk_status s = launch(seq_range_kernel<D, T>, dim3(static_cast<unsigned>(a.batch), 2, z), 256, 0, st,
+                                   static_cast<const T*>(V), static_cast<const T*>(dO), range, a);
+        if (s != WK_OK) return s;
+      }
+    }
+    float* slots = reinterpret_cast<float*>(rest);
     if (a.total_q > 0) {
-      const wk_status s = one<D, T, false>(q, delta, slots, dQ, nullptr);
+      const wk_status s = one<D, T, false>(q, delta, range, slots, dQ, nullptr);
       if (s != WK_OK) return s;
     }
     if (a.total_kv > 0) {
-      const wk_status s = one<D, T, true>(k, delta, slots, dK, dV);
+      const wk_status s = one<D, T, true>(k, delta, range, slots, dK, dV);
       if (s != WK_OK) return s;
       if (a.kv_lens) {
         // a block for each 16 KB that a sequence would have to clear if it were all padding
@@ -403,7 +425,7 @@ wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, int64_t* 
   const wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
   const int64_t forward = forward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d, false);
-  *bytes = backward ? std::max(forward, backward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d)) : forward;
+  *bytes = backward ? std::max(forward, backward_ws(make_args(*cfg, nullptr, nullptr, nullptr, nullptr), cfg->d, cfg->dtype)) : forward;
   return WK_OK;
 }
 

@@ -1,6 +1,6 @@
 """Attention over behaviour sequences on the GPU where the values are far apart, tiny, huge, zero or not finite:
-8-bit rows with powers of two of every size, NaN bytes, single infinite scores, fp16
-gradients.
+8-bit rows with powers of two of every size, NaN bytes, single infinite scores, fp16 gradients of small and of large
+losses.
 
 Bounds, with u half a step of the 16-bit type and e_j = ES + 2^-23 d sum |q k_j| scale of each score (seq_util):
   8-bit caches  key j's weight is off by P_j (u + 2 e_j), and every weight by the row sum's sum_j P_j e_j. Weights
@@ -227,7 +227,7 @@ def _grad_bounds(q, k, v, g, scale):
     """{name: (reference, bound)} of one sequence, fp16 (see the head of this file)."""
     n, hq, d = q.shape
     L, hk, _ = k.shape
-    u, least = 2.0 ** -11 / 2, 2.0 ** -24
+    u, least = U.half_step(torch.float16), 2.0 ** -24
     ke, ve = U.expand(k, hq), U.expand(v, hq)
     S = np.einsum("nhd,lhd->nhl", q, ke) * scale
     e = (U.ES + 2.0 ** -23 * d * np.einsum("nhd,lhd->nhl", np.abs(q), np.abs(ke)) * scale).max(axis=2, keepdims=True)
@@ -269,6 +269,27 @@ def _check_grads(j, grads, scale, names=("dQ", "dK", "dV")):
         qa, ka = qa + n, ka + kv
 
 
+SMALL = [
+    # rows, keys, q heads, kv heads, d
+    ([64, 5], [2048, 300], 2, 1, 128),
+    ([16], [15000], 2, 1, 64),
+    ([40, 300], [130, 4100], 1, 1, 160),
+    ([300, 7], [90, 1], 4, 2, 32),
+]
+
+
+@pytest.mark.parametrize("power", [-7, -10, -13])
+@pytest.mark.parametrize("n,kv,hq,hk,d", SMALL)
+def test_gradients_of_a_small_loss(n, kv, hq, hk, d, power):
+    """dO of the size that a mean over a batch gives."""
+    j = Jagged(n, kv, hq, hk, d, "f16", behind=0)
+    j.g *= 2.0 ** power
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    _check_grads(j, grads, 1 / np.sqrt(d))
+
+
 def test_weights_below_halfs_normal_range_reach_dv():
     """Keys with softmax weights of 2^-16 to 2^-22: their value gradients are ordinary numbers."""
     j = Jagged([60], [4000], 1, 1, 64, "f16", behind=0)
@@ -279,3 +300,49 @@ def test_weights_below_halfs_normal_range_reach_dv():
     grads = j.backward(O, L)
     _ok()
     _check_grads(j, grads, 1 / 8, ("dV",))
+
+
+@pytest.mark.parametrize("n,kv,qk,vs,gs", [([2, 3], [4, 100], 2.0 ** -7, 512.0, 4096.0),
+                                           ([40], [200], 2.0 ** -6, 1024.0, 8192.0),
+                                           ([200, 70], [600, 1000], 2.0 ** -8, 4096.0, 8192.0)])
+def test_gradients_of_a_large_loss(n, kv, qk, vs, gs):
+    """dO V^T beyond fp16's largest value, gradients within it."""
+    j = Jagged(n, kv, 2, 1, 128, "f16", behind=0)
+    for t, s in ((j.q, qk), (j.k, qk), (j.v, vs), (j.g, gs)):
+        t *= s
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    ref = np.abs(U.f64(j.g)).max() * np.abs(U.f64(j.v)).max()
+    assert ref > 65504
+    _check_grads(j, grads, 1 / np.sqrt(128))
+
+
+def test_rows_with_losses_of_different_size():
+    """Each row's gradient goes by its own dO; a row without any has none."""
+    j = Jagged([50, 20], [1500, 100], 2, 1, 64, "f16", behind=0)
+    w = torch.exp2(torch.arange(70, device="cuda") % 13 * -1.0)
+    w[::9] = 0.0
+    j.g = (j.g.float() * w[:, None, None]).half()
+    O, L = j.forward()
+    grads = j.backward(O, L)
+    _ok()
+    _check_grads(j, grads, 1 / 8)
+    assert (grads[0][::9] == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_a_poisoned_neighbour_of_small_gradients(dt):
+    """NaN and infinities in one sequence's values and output gradients leave the others' gradients as they were."""
+    j = Jagged([70, 10, 65], [100, 37, 213], 2, 2, 64, dt)
+    j.g *= 2.0 ** -10
+    clean = j.forward()
+    cg = j.backward(*clean)
+    for bad in (float("nan"), float("inf")):
+        j.v[j.kv_off[1]:j.kv_off[2]] = bad
+        j.g[j.q_off[1]:j.q_off[2]] = bad
+        grads = j.backward(*j.forward())
+        _ok()
+        for a, b, off in zip(cg, grads, (j.q_off, j.kv_off, j.kv_off)):
+            for lo, hi in ((off[0], off[1]), (off[2], off[3])):
+                assert torch.equal(a[lo:hi], b[lo:hi])
