@@ -512,7 +512,7 @@ WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_wha
  * their weights for it are 0.)
  *
  * Offsets, lengths and page tables are on the device, so their content is checked there: where they
- * point outside the tensors, or a sequence is longer than max_q / max_kv says, the access is
+ * point outside the tensors, or a sequence is longer than max_q / max_kv (0 too) says, the access is
  * left out, the result is not valid, and wk_device_status returns WK_ERR_DEVICE.
  *
  * Arithmetic: 16-bit inputs and outputs; products accumulate in fp32; scores, softmax statistics

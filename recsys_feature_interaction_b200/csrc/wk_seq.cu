@@ -164,7 +164,7 @@ int64_t slot_bytes(int r, int d, int64_t pieces) {
   return pieces * static_cast<int64_t>(sizeof(SeqNote)) + 2 * pieces * r * (d + 2) * 4;
 }
 
-bool rows_cut(const SeqArgs& a) { return a.max_kv > kUncut * kRowsKB; }
+bool rows_cut(const SeqArgs& a) { return a.max_q > 0 && a.max_kv > kUncut * kRowsKB; }
 // Bytes of partial results.
 int64_t rows_ws(const SeqArgs& a, int d, bool q8) {
   const int nq = rows_nq(a);
@@ -382,6 +382,10 @@ struct RunBackward {
   }
 };
 
+// Blocks of the copies per (sequence, key head, K or V); one at least, which sees sequences that are
+// longer than a maximum of 0.
+int32_t copy_chunks(int32_t most) { return std::max(1, (most + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS); }
+
 struct RunWrite {
   const wk_cache& c;
   const void *K, *V;
@@ -434,7 +438,7 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
                            void* workspace, int64_t workspace_bytes, wk_stream_t stream) {
   wk_status s = check_config(cfg);
   if (s != WK_OK) return s;
-  if (cfg->batch == 0 || cfg->total_q == 0 || cfg->max_q == 0) return WK_OK;
+  if (cfg->batch == 0 || cfg->total_q == 0) return WK_OK;
   const bool keys = cfg->total_kv > 0;
   if (!Q || !O || !q_off || !kv_off || (keys && (!K || !V)) || !al16(Q) || !al16(K) || !al16(V) || !al16(O) ||
       !al4(q_off) || !al4(kv_off) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
@@ -505,7 +509,7 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
                       v_stride, dtype, 0.f};
   s = check_config(&cfg);
   if (s != WK_OK) return s;
-  if (batch == 0 || total_new == 0 || max_new == 0) return WK_OK;
+  if (batch == 0 || total_new == 0) return WK_OK;
   if (!K || !V || !new_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
       !al4(new_off) || !al4(table) || !al4(kv_lens))
     return WK_ERR_INVALID_ARG;
@@ -518,7 +522,7 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
   const Bytes read[] = {{K, extent(total_new, a.k_stride, cfg.kv_heads, cfg.d)},
                         {V, extent(total_new, a.v_stride, cfg.kv_heads, cfg.d)}};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
-  const int32_t chunks = (max_new + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
+  const int32_t chunks = copy_chunks(max_new);
   const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
   if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
   DevInfo* dv = nullptr;
@@ -536,7 +540,7 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   if (s != WK_OK) return s;
   if (batch < 0 || total < 0 || total > kMaxRows || max_kv < 0 || table_width < 0) return WK_ERR_INVALID_ARG;
   if (!type16(dtype) || (cache->dtype != WK_E4M3 && cache->dtype != dtype)) return WK_ERR_UNSUPPORTED;
-  if (batch == 0 || total == 0 || max_kv == 0) return WK_OK;
+  if (batch == 0 || total == 0) return WK_OK;
   if (!K || !V || !out_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
       !al4(out_off) || !al4(table) || !al4(kv_lens))
     return WK_ERR_INVALID_ARG;
@@ -549,7 +553,7 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
   SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
   cache_args(&a, *cache, table, table_width);
-  const int32_t chunks = (max_kv + SEQ_COPY_ROWS - 1) / SEQ_COPY_ROWS;
+  const int32_t chunks = copy_chunks(max_kv);
   const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
   if (grid > INT32_MAX) return WK_ERR_UNSUPPORTED;
   DevInfo* dv = nullptr;
@@ -579,7 +583,7 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   wk_status s = wk_cache_attention_workspace(cache, cfg, &need);
   if (s != WK_OK) return s;
   if (table_width < 0) return WK_ERR_INVALID_ARG;
-  if (cfg->batch == 0 || cfg->total_q == 0 || cfg->max_q == 0) return WK_OK;
+  if (cfg->batch == 0 || cfg->total_q == 0) return WK_OK;
   if (!Q || !O || !q_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(Q) || !al16(O) ||
       !al4(q_off) || !al4(table) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
     return WK_ERR_INVALID_ARG;
