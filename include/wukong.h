@@ -545,7 +545,7 @@ WK_API wk_status wk_xattn_workspace(const wk_xattn_config* cfg, int backward, in
  * over K, V [total_kv, kv_heads, d]. q_off, kv_off: batch + 1 offsets. kv_lens: batch lengths, of
  * sequence b's rows the first kv_lens[b] are keys (padded batches: kv_off[b] = b * L), or NULL:
  * all are. V may be K (shared keys and values). O, lse and the workspace must not overlap the
- * inputs or one another. Pointers 16-byte aligned, the offsets 4-byte. Asynchronous on `stream`;
+ * inputs (offsets and lengths among them) or one another. Pointers 16-byte aligned, the offsets 4-byte. Asynchronous on `stream`;
  * may be captured. Errors: WK_ERR_INVALID_ARG (NULL, misaligned, negative or inconsistent sizes,
  * workspace too small, overlapping buffers), WK_ERR_UNSUPPORTED (d, dtype, a stride that is no
  * multiple of 8), WK_ERR_CUDA. */
@@ -586,7 +586,8 @@ typedef struct {
  * LAST ones of its kv_lens[b] positions (kv_lens counts them). table [batch, table_width] int32.
  * A 16-bit cache takes tokens of its own type. Two tokens must not go to one place (a page that two
  * sequences append to): what that row then holds is one of the two, or a mix. Entries of the table
- * that no new token needs are not read. The cache's tensors and the tokens must not overlap. Errors:
+ * that no new token needs are not read. The cache's tensors must not overlap one another, the
+ * tokens, offsets, lengths or the table. Errors:
  * WK_ERR_INVALID_ARG, WK_ERR_UNSUPPORTED (d, page_size, dtypes), WK_ERR_CUDA. */
 WK_API wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, int64_t k_stride,
                                 int64_t v_stride, wk_dtype dtype, const int32_t* new_off, const int32_t* table,

@@ -40,6 +40,9 @@ struct Bytes {
   int64_t n;
 };
 
+// `n` int32 values of device memory (offsets, lengths, a table).
+Bytes ints(const int32_t* p, int64_t n) { return {p, n * 4}; }
+
 // Whether something written lies over something read, or over something else written.
 template <int W, int R>
 bool overlap(const Bytes (&written)[W], const Bytes (&read)[R]) {
@@ -453,7 +456,10 @@ wk_status wk_xattn_forward(const wk_xattn_config* cfg, const void* Q, const void
                            {workspace, need}};
   const Bytes read[] = {{Q, extent(cfg->total_q, a.q_stride, cfg->q_heads, cfg->d)},
                         {K, extent(cfg->total_kv, a.k_stride, cfg->kv_heads, cfg->d)},
-                        {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)}};
+                        {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)},
+                        ints(q_off, cfg->batch + int64_t{1}),
+                        ints(kv_off, cfg->batch + int64_t{1}),
+                        ints(kv_lens, cfg->batch)};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
@@ -486,7 +492,10 @@ wk_status wk_xattn_backward(const wk_xattn_config* cfg, const void* Q, const voi
                         {V, extent(cfg->total_kv, a.v_stride, cfg->kv_heads, cfg->d)},
                         {O, qb},
                         {dO, qb},
-                        {lse, cfg->total_q * cfg->q_heads * 4}};
+                        {lse, cfg->total_q * cfg->q_heads * 4},
+                        ints(q_off, cfg->batch + int64_t{1}),
+                        ints(kv_off, cfg->batch + int64_t{1}),
+                        ints(kv_lens, cfg->batch)};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   if (!rows && !keys) return WK_OK;
   DevInfo* dv = nullptr;
@@ -520,7 +529,10 @@ wk_status wk_cache_write(const wk_cache* cache, const void* K, const void* V, in
                            {cache->K_exp, cache_rows(*cache)},
                            {cache->V_exp, cache_rows(*cache)}};
   const Bytes read[] = {{K, extent(total_new, a.k_stride, cfg.kv_heads, cfg.d)},
-                        {V, extent(total_new, a.v_stride, cfg.kv_heads, cfg.d)}};
+                        {V, extent(total_new, a.v_stride, cfg.kv_heads, cfg.d)},
+                        ints(new_off, batch + int64_t{1}),
+                        ints(table, static_cast<int64_t>(batch) * table_width),
+                        ints(kv_lens, batch)};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   const int32_t chunks = copy_chunks(max_new);
   const int64_t grid = static_cast<int64_t>(batch) * chunks * cache->kv_heads * 2;
@@ -548,7 +560,10 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   const Bytes read[] = {{cache->K, cache_bytes(*cache)},
                         {cache->V, cache_bytes(*cache)},
                         {cache->K_exp, cache_rows(*cache)},
-                        {cache->V_exp, cache_rows(*cache)}};
+                        {cache->V_exp, cache_rows(*cache)},
+                        ints(out_off, batch + int64_t{1}),
+                        ints(table, static_cast<int64_t>(batch) * table_width),
+                        ints(kv_lens, batch)};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   wk_xattn_config cfg{batch, cache->kv_heads, cache->kv_heads, cache->d, 0, max_kv, 0, total, 0, 0, 0, dtype, 0.f};
   SeqArgs a = make_args(cfg, nullptr, out_off, kv_lens, nullptr);
@@ -598,7 +613,10 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
                         {cache->K, cache_bytes(*cache)},
                         {cache->V, cache_bytes(*cache)},
                         {cache->K_exp, cache_rows(*cache)},
-                        {cache->V_exp, cache_rows(*cache)}};
+                        {cache->V_exp, cache_rows(*cache)},
+                        ints(q_off, cfg->batch + int64_t{1}),
+                        ints(table, static_cast<int64_t>(cfg->batch) * table_width),
+                        ints(kv_lens, cfg->batch)};
   if (overlap(written, read)) return WK_ERR_INVALID_ARG;
   DevInfo* dv = nullptr;
   s = dev_info(&dv);
