@@ -610,7 +610,8 @@ WK_API wk_status wk_cache_attention_workspace(const wk_cache* cache, const wk_xa
  * tokens, row i of n sees the keys at positions <= kv_lens[b] - n + i (its own, already written,
  * among them); causal == 0: every row sees every key (candidates over a history). cfg->kv_heads and
  * cfg->d are the cache's; cfg->dtype is the type of Q and O (a 16-bit cache's own). Keys and values
- * of an 8-bit cache enter with the values they stand for. table, kv_lens as wk_cache_write; O, lse,
+ * of an 8-bit cache enter with the values they stand for. A cache without pages and a table of width 0
+ * hold empty histories. table, kv_lens as wk_cache_write; O, lse,
  * workspace, errors as wk_xattn_forward. */
 WK_API wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, const void* Q,
                                     const int32_t* q_off, const int32_t* table, int32_t table_width,

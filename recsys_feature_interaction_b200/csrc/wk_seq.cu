@@ -204,13 +204,15 @@ bool map_tokens(const DevInfo* dv, CUtensorMap* m, const void* base, const void*
                   bw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The rows of a 16-bit cache as a 2-D map (d, rows) with boxes of one page.
+// The rows of a 16-bit cache as a 2-D map (d, rows) with boxes of one page. Of no pages it is a map
+// over `any`, and not used.
 template <typename T>
-bool map_pages(const DevInfo* dv, CUtensorMap* m, const void* base, int d, int64_t rows, int bw, int page) {
-  const uint64_t dims[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows)};
+bool map_pages(const DevInfo* dv, CUtensorMap* m, const void* base, const void* any, int d, int64_t rows, int bw,
+               int page) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(d), static_cast<uint64_t>(std::max<int64_t>(rows, 1))};
   const uint64_t strides[1] = {static_cast<uint64_t>(d) * 2};
   const uint32_t box[2] = {static_cast<uint32_t>(bw), static_cast<uint32_t>(page)};
-  return make_map(dv, m, tmap_dtype<T>(), 2, base, dims, strides, box,
+  return make_map(dv, m, tmap_dtype<T>(), 2, rows > 0 ? base : any, dims, strides, box,
                   bw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
@@ -230,8 +232,8 @@ wk_status run_tile(const DevInfo* dv, const void* Q, const void* K, const void* 
       return WK_ERR_UNSUPPORTED;
   } else if (SRC == SEQ_PAGED16) {
     const int64_t rows = (static_cast<int64_t>(a.num_pages) * a.kv_heads) << a.page_shift;
-    if (rows > INT32_MAX || !map_pages<T>(dv, &mk, K, D, rows, C::BW, 1 << a.page_shift) ||
-        !map_pages<T>(dv, &mv, V, D, rows, C::BW, 1 << a.page_shift))
+    if (rows > INT32_MAX || !map_pages<T>(dv, &mk, K, Q, D, rows, C::BW, 1 << a.page_shift) ||
+        !map_pages<T>(dv, &mv, V, Q, D, rows, C::BW, 1 << a.page_shift))
       return WK_ERR_UNSUPPORTED;
   }
   auto fn = seq_tile_kernel<D, T, SRC>;
@@ -553,7 +555,7 @@ wk_status wk_cache_read(const wk_cache* cache, const int32_t* table, int32_t tab
   if (batch < 0 || total < 0 || total > kMaxRows || max_kv < 0 || table_width < 0) return WK_ERR_INVALID_ARG;
   if (!type16(dtype) || (cache->dtype != WK_E4M3 && cache->dtype != dtype)) return WK_ERR_UNSUPPORTED;
   if (batch == 0 || total == 0) return WK_OK;
-  if (!K || !V || !out_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(K) || !al16(V) ||
+  if (!K || !V || !out_off || (!table && table_width > 0) || !kv_lens || !al16(K) || !al16(V) ||
       !al4(out_off) || !al4(table) || !al4(kv_lens))
     return WK_ERR_INVALID_ARG;
   const Bytes written[] = {{K, total * cache->kv_heads * cache->d * 2}, {V, total * cache->kv_heads * cache->d * 2}};
@@ -599,7 +601,7 @@ wk_status wk_cache_attention(const wk_cache* cache, const wk_xattn_config* cfg, 
   if (s != WK_OK) return s;
   if (table_width < 0) return WK_ERR_INVALID_ARG;
   if (cfg->batch == 0 || cfg->total_q == 0) return WK_OK;
-  if (!Q || !O || !q_off || !table || !kv_lens || table_width < 1 || cache->num_pages < 1 || !al16(Q) || !al16(O) ||
+  if (!Q || !O || !q_off || (!table && table_width > 0) || !kv_lens || !al16(Q) || !al16(O) ||
       !al4(q_off) || !al4(table) || !al4(kv_lens) || !al4(lse) || !al16(workspace) || workspace_bytes < 0)
     return WK_ERR_INVALID_ARG;
   if (need > workspace_bytes || (need > 0 && !workspace)) return WK_ERR_INVALID_ARG;

@@ -52,3 +52,41 @@ def test_a_maximum_of_zero_is_told(bits):
             assert (t == 7.0).all()
     # a step with fewer bytes of workspace than the smallest of a longer one
     assert wk.wk_xattn_workspace(j.q, j.k, 2, 0, 700) == 0
+
+
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("bits,dt", [(8, "bf16"), (8, "f16"), (16, "bf16"), (16, "f16")])
+@pytest.mark.parametrize("pages,width", [(0, 0), (0, 3), (4, 0)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_cache_that_holds_nothing_yet(causal, pages, width, bits, dt, n):
+    """Empty histories over no pages, or a table without columns: zeros, as over no keys at all. A history that is
+    not empty has no place there, and is told."""
+    gen = torch.Generator().manual_seed(2)
+    kind = torch.float8_e4m3fn if bits == 8 else DT[dt]
+    cache = {x: torch.zeros(pages, 2, 16, 64, dtype=torch.uint8 if bits == 8 else kind, device="cuda").view(kind)
+             for x in ("K", "V")}
+    if bits == 8:
+        cache.update({x: torch.zeros(pages, 2, 16, dtype=torch.uint8, device="cuda") for x in ("K_exp", "V_exp")})
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = _rand(gen, DT[dt], n + 1, 4, 64)
+    off = U.offsets([n, 1])
+    for most, keys in ((0, 0), (900, 0), (900, 5)):
+        O, lse = torch.full_like(q, 7.0), torch.full((n + 1, 4), 7.0, device="cuda")
+        need = wk.wk_cache_attention_workspace(cache, q, 2, n, most)
+        ws = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
+        lens[0] = keys
+        wk.wk_cache_attention(cache, q, O, off, table, lens, n, most, causal=causal, lse=lse, workspace=ws)
+        if keys:
+            assert _status() == wk.WK_ERR_DEVICE
+            assert (O[n:] == 0).all()
+        else:
+            _ok()
+            assert (O == 0).all() and torch.isneginf(lse).all()
+        K, V = (torch.full((7, 2, 64), 7.0, dtype=DT[dt], device="cuda") for _ in range(2))
+        wk.wk_cache_read(cache, table, lens, U.offsets([5, 2]), K, V, most)
+        if keys:
+            assert _status() == wk.WK_ERR_DEVICE
+        else:
+            _ok()
+        assert (K == 7.0).all() and (V == 7.0).all()
