@@ -6,7 +6,6 @@ uses the caller's CUDA context when there is one.
 """
 import os
 import subprocess
-import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,12 +28,27 @@ def _object(source):
 
 
 def _older(target, source):
-    """Whether `target` is missing or older than the source, its headers or the public header."""
-    if not os.path.exists(target):
+    """Whether `target` is missing, older than the source, its headers or the public header, or made with other
+    flags than today's."""
+    if not os.path.exists(target) or _flags_changed(source):
         return True
     t = os.path.getmtime(target)
     deps = [os.path.join(CSRC, f) for f in [source] + SOURCES[source]] + [os.path.join(INCLUDE, "wukong.h")]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _flag_line():
+    """The flags as a line; without the include paths, which go by where the tree lies."""
+    return "flags: " + " ".join(f for f in nvcc_flags() if not f.startswith("-I"))
+
+
+def _flags_changed(source):
+    """Whether the log of the source's object, which begins with its flags, names others."""
+    try:
+        with open(_object(source) + ".log") as log:
+            return log.readline().rstrip("\n") != _flag_line()
+    except FileNotFoundError:
+        return False
 
 
 def _stale():
@@ -57,10 +71,12 @@ def build(force=False, verbose=False):
     for s in SOURCES:
         if force or _older(_object(s), s):
             with open(_object(s) + ".log", "w") as log:
+                log.write(_flag_line() + "\n")
+                log.flush()
                 cmd = ["nvcc", "-c"] + nvcc_flags() + ["-o", _object(s), os.path.join(CSRC, s)]
                 running.append((s, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)))
     failed = [s for s, p in running if p.wait() != 0]
-    logs = "".join(open(_object(s) + ".log").read() for s in (failed or SOURCES))
+    logs = "".join(open(_object(s) + ".log").read() for s in (failed or SOURCES) if os.path.exists(_object(s) + ".log"))
     if failed:
         for s in failed:
             if os.path.exists(_object(s)):
@@ -77,6 +93,10 @@ def build(force=False, verbose=False):
     return LIB
 
 
+def main():
+    """python -m recsys_feature_interaction_b200.build: compiles everything anew."""
+    print(build(force=True))
+
+
 if __name__ == "__main__":
-    build(force="force" in sys.argv[1:])
-    print(LIB)
+    main()
