@@ -18,9 +18,10 @@
 // the row sees, beside the row sum of 2^(s - m). So what a row gives does not depend on the size of
 // rows that have no weight. (Multiplied onto the converted values, relative to the largest row met, it
 // lost those 2^25 below it, and took two more instructions a pair against one exponential a weight.)
-// bf16 queries are scaled by a power of two of their own row, so that they are exact in fp16 down to
-// 2^-39 of the row's largest. (Shifting e4m3's bits into bf16's fields took four instructions a pair
-// and made the kernel wait for the ALU: 86 us at 64 sequences of up to 15,000 keys.)
+// bf16 queries are scaled by a power of two of their own row into fp16: elements down to 2^-31 of the
+// row's largest are exact, smaller ones round to steps of 2^-38 of it. (Shifting e4m3's bits into bf16's
+// fields instead, which has no such limit, took four instructions a pair and made the kernel wait for
+// the ALU: 86 us at 64 sequences of up to 15,000 keys, where this takes 62.)
 #pragma once
 
 #include "seq_args.cuh"
@@ -30,11 +31,13 @@ namespace wk {
 constexpr int SEQ_ROWS_WARPS = 4;
 constexpr int SEQ_ROWS_THREADS = 32 * SEQ_ROWS_WARPS;
 // Blocks per SM, and so the registers of a thread. More warps hide more of a step's dependent
-// instructions, down to where registers spill: one new token over 64 8-bit caches of up to 15,000
-// keys, d = 128, takes 72 us with two blocks, 69 with three, 66 with four (and 16 keys a step, so
-// that four fit); 16 rows of a wide head need the registers of two.
+// instructions, as long as registers do not spill (more than a few dozen bytes). One new token over 64
+// caches of up to 15,000 keys, with 2, 3, 4 blocks (bytes spilled):
+//   8 bits   d = 128: 77, 64, 63 us (0, 0, 50)     d = 160: 84, 73, 98 us (0, 0, 290)
+//   16 bits  d = 128: 88, 85, 98 us (0, 0, 306)    d = 160: 103, 115, 168 us (0, 226, 646)
+// 16 rows of a wide head need the registers of two.
 constexpr int seq_rows_occupancy(int d, int nq, bool q8) {
-  return nq == 2 ? (d >= 128 ? 2 : 3) : (d <= 64 || (d == 128 && q8) ? 4 : 3);
+  return nq == 2 ? (d >= 128 ? 2 : 3) : (d <= 64 || (d == 128 && q8) ? 4 : d == 160 && !q8 ? 2 : 3);
 }
 
 // 16-byte, 8-byte or 4-byte load of data that is read once.
