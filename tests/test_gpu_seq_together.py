@@ -123,3 +123,43 @@ def test_two_branches_of_one_graph(bits, dt):
         _ok()
         for a, b in zip(got, want):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_a_captured_training_step_on_new_values(dt):
+    """A padded training step, captured; replayed with another loss, other lengths and other values, it gives the
+    gradients of the eager calls on them."""
+    gen = torch.Generator().manual_seed(4)
+    j = Jagged([30, 1, 65], [700, 40, 300], 4, 2, 64, dt, behind=0)
+    lens = torch.tensor([650, 0, 300], dtype=torch.int32, device="cuda")
+    ws = j.workspace(True)
+    out = [torch.empty_like(j.q), torch.empty(j.q.shape[:2], device="cuda"),
+           *(torch.empty(t.shape, dtype=t.dtype, device="cuda") for t in (j.q, j.k, j.v))]
+
+    def step():
+        wk.wk_xattn_forward(j.q, j.k, j.v, out[0], j.q_off, j.kv_off, 65, 700, kv_lens=lens, lse=out[1], workspace=ws)
+        wk.wk_xattn_backward(j.q, j.k, j.v, out[0], out[1], j.g, *out[2:], j.q_off, j.kv_off, 65, 700, kv_lens=lens,
+                             workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    for i, (size, use) in enumerate((((1.0), [650, 0, 300]), (2.0 ** -9, [1, 40, 129]), (2.0 ** 5, [700, 0, 0]))):
+        lens.copy_(torch.tensor(use, dtype=torch.int32))
+        for t in (j.q, j.k, j.v):
+            t.copy_(_rand(gen, j.dt, *t.shape))
+        j.g.copy_(_rand(gen, j.dt, *j.g.shape, std=size))
+        for t in out:
+            t.fill_(7.0)
+        graph.replay()
+        _ok()
+        got = [t.clone() for t in out]
+        for t in out:
+            t.fill_(5.0)
+        step()
+        _ok()
+        for a, b in zip(got, out):
+            assert torch.equal(a, b), i
+        if size == 1.0 or dt == "bf16":
+            j.check(out[0], out[1], out[2:], lens=use)

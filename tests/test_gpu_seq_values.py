@@ -31,15 +31,10 @@ def _lib(cuda_device):
 
 # ------------------------------------------------------------------ 8-bit rows of every size
 
-def _raw(c, b):
-    """(k, k exponents, v, v exponents) of sequence b, e4m3 values and powers in float64."""
-    pos = np.arange(c.kv[b])
-    page, row = c.host_table[b][pos // c.page], pos % c.page
-    out = []
-    for name in ("K", "V"):
-        out.append(U.f64(c.cache[name].float())[page, :, row])
-        out.append(np.ldexp(1.0, U.f64(c.cache[name + "_exp"]).astype(int)[page, :, row] - 127))
-    return out
+def _held(c):
+    """{name: (e4m3 values, powers of two)} of the whole cache in float64."""
+    return {name: (U.f64(c.cache[name].float()),
+                   np.ldexp(1.0, c.cache[name + "_exp"].cpu().numpy().astype(int) - 127)) for name in ("K", "V")}
 
 
 def _set(c, b, pos, name, values=None, exp=None):
@@ -55,12 +50,17 @@ def _set(c, b, pos, name, values=None, exp=None):
 
 
 def _check8(c, q, n, O, causal):
-    at = 0
+    at, held = 0, _held(c)
     u, d = U.half_step(c.dt), c.d
     least = torch.finfo(c.dt).smallest_normal * torch.finfo(c.dt).eps
     for b, m in enumerate(n):
-        x = [U.expand(t, q.shape[1]) for t in _raw(c, b)[:1] + [_raw(c, b)[2]]]
-        kp, vp = (np.repeat(t, q.shape[1] // c.hk, axis=1) for t in (_raw(c, b)[1], _raw(c, b)[3]))
+        if m == 0 or c.kv[b] == 0:
+            assert (O[at:at + m] == 0).all()
+            at += m
+            continue
+        pos = np.arange(c.kv[b])
+        page, row = c.host_table[b][pos // c.page], pos % c.page
+        x, (kp, vp) = ([U.expand(held[name][i][page, :, row], q.shape[1]) for name in ("K", "V")] for i in (0, 1))
         k, v = x[0] * kp[..., None], x[1] * vp[..., None]
         qq = U.f64(q[at:at + m])
         seen = np.array([max(0, c.kv[b] - m + i + 1) if causal else c.kv[b] for i in range(m)])
@@ -173,6 +173,22 @@ def test_value_rows_of_every_size(causal, n, kv, d, page, dt):
     O, _ = _attend(c, q, U.offsets(n), max(n), causal)
     _ok()
     _check8(c, q, n, O, causal)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,d", [(2, 64), (20, 64), (20, 160)])
+def test_hundreds_of_cached_sequences(rows, d, dt):
+    """More units than blocks of the grid, of no key to several blocks of keys, rows of every size."""
+    gen = torch.Generator().manual_seed(8)
+    r = np.random.RandomState(8)
+    n = [int(x) for x in r.randint(0, rows + 1, 400)]
+    kv = [int(x) for x in np.maximum(r.choice([0, 20, 130, 700], 400) - r.randint(0, 20, 400), 0)]
+    c = Cached(kv, 2, d, dt, 16, 8)
+    c.cache["V_exp"][:] = torch.randint(80, 124, c.cache["V_exp"].shape, generator=gen).to(torch.uint8).cuda()
+    q = _rand(gen, c.dt, sum(n), 4, d, std=0.5)
+    O, _ = _attend(c, q, U.offsets(n), rows, True)
+    _ok()
+    _check8(c, q, n, O, True)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
