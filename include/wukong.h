@@ -519,7 +519,9 @@ WK_API wk_status wk_whale_fusion_ffn(const void* Hw, const void* A, const wk_wha
  * and lse are fp32 (lse off by up to 1e-4, the error of one exponential); the softmax weights and the
  * gradients of the scores are rounded to the 16-bit type as tensor-core operands. fp16 gradients take
  * a power of two out first, from the norms of dO and V, so that a loss of any size uses fp16's range
- * from the top. Results do not depend on the order in which blocks run. */
+ * from the top. Calls of few rows (at most 16 query rows times shared heads per sequence) over an 8-bit
+ * cache hold weights and queries in fp16, whatever the dtype: weights together with their value row's
+ * power of two, bf16 query rows relative to their largest element, exact down to 2^-31 of it. Results do not depend on the order in which blocks run. */
 
 typedef struct {
   int32_t batch;               /* sequences, >= 0 */
