@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
               float p[4], s[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                p[e] = whale_ex2(fmaf(__uint_as_float(t1[4 * c4 + e]), scale_log2, UP - lv[e]));
+                p[e] = seq_ex2(fmaf(__uint_as_float(t1[4 * c4 + e]), scale_log2, UP - lv[e]));
                 s[e] = p[e] * ((__uint_as_float(t2[4 * c4 + e]) - dv[e]) * ds_in);
               }
               pp[2 * c4] = Half16<T>::pack2(p[0], p[1]);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
               const int valid = u.len - j * a.block - half * (C::YB / 2) - at;
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                t1[c] = __float_as_uint(whale_ex2(fmaf(__uint_as_float(t1[c]), scale_log2, -lse2)));
+                t1[c] = __float_as_uint(seq_ex2(fmaf(__uint_as_float(t1[c]), scale_log2, -lse2)));
               if (valid < 32) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)

@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
             const uint32_t gp = g - 1u;
             if (ok) ok = seq_wait(&p_empty[gp % C::NS], (gp / C::NS) & 1u, status);
             tc_fence_after();
-            const float factor = need ? whale_ex2((FAR ? wprev : mprev) - wnew) : 1.f;
+            const float factor = need ? seq_ex2((FAR ? wprev : mprev) - wnew) : 1.f;
             if (warp_on) {
 #pragma unroll 1
               for (int cc = 0; cc < D / 16; ++cc) {
@@ -698,17 +698,17 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
                 const float4 x = *reinterpret_cast<const float4*>(vexp + at + 4 * c4);
                 const float s[4] = {__uint_as_float(sr[4 * c4]), __uint_as_float(sr[4 * c4 + 1]),
                                     __uint_as_float(sr[4 * c4 + 2]), __uint_as_float(sr[4 * c4 + 3])};
-                sum[0] = seq_add2(sum[0], make_float2(whale_ex2(s[0] + nm), whale_ex2(s[1] + nm)));
-                sum[1] = seq_add2(sum[1], make_float2(whale_ex2(s[2] + nm), whale_ex2(s[3] + nm)));
-                pk[2 * c4] = Half16<T>::pack2(whale_ex2(s[0] + (x.x + nw)), whale_ex2(s[1] + (x.y + nw)));
-                pk[2 * c4 + 1] = Half16<T>::pack2(whale_ex2(s[2] + (x.z + nw)), whale_ex2(s[3] + (x.w + nw)));
+                sum[0] = seq_add2(sum[0], make_float2(seq_ex2(s[0] + nm), seq_ex2(s[1] + nm)));
+                sum[1] = seq_add2(sum[1], make_float2(seq_ex2(s[2] + nm), seq_ex2(s[3] + nm)));
+                pk[2 * c4] = Half16<T>::pack2(seq_ex2(s[0] + (x.x + nw)), seq_ex2(s[1] + (x.y + nw)));
+                pk[2 * c4 + 1] = Half16<T>::pack2(seq_ex2(s[2] + (x.z + nw)), seq_ex2(s[3] + (x.w + nw)));
               }
             } else
 #pragma unroll
             for (int c2 = 0; c2 < KB / 4; ++c2) {
               const float2 x =
                   seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
-              const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(whale_ex2(x.x), whale_ex2(x.y));
+              const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(seq_ex2(x.x), seq_ex2(x.y));
               sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
               pk[c2] = Half16<T>::pack2(p.x, p.y);
             }
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
           float lsum = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           if (mnew == -INFINITY) lsum = 0.f;  // no key seen yet
           if (mh != mh) lsum = mh;            // a NaN score: the polynomial would lose it
-          l = (m == -INFINITY ? l * 0.f : l * whale_ex2(m - mnew)) + lsum;
+          l = (m == -INFINITY ? l * 0.f : l * seq_ex2(m - mnew)) + lsum;
           m = mnew;
           wm = wnew;
         }
@@ -738,11 +738,11 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
         float between = 1.f;
         if constexpr (FAR) {
           const float wf = wrow[(gl & 1u) * R + row];
-          between = wf == -INFINITY ? 0.f : whale_ex2(0.5f * (wf - mz));
+          between = wf == -INFINITY ? 0.f : seq_ex2(0.5f * (wf - mz));
         }
         float lt = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) lt += lrow[x * R + row] * whale_ex2(mrow[x * R + row] - mz);
+        for (int x = 0; x < 2; ++x) lt += lrow[x * R + row] * seq_ex2(mrow[x * R + row] - mz);
         named_bar(pair_id, 64);  // before the next unit overwrites them
         if (ok) ok = seq_wait(&p_empty[gl % C::NS], (gl / C::NS) & 1u, status);
         tc_fence_after();

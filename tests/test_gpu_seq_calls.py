@@ -90,3 +90,26 @@ def test_a_cache_that_holds_nothing_yet(causal, pages, width, bits, dt, n):
         else:
             _ok()
         assert (K == 7.0).all() and (V == 7.0).all()
+
+
+def test_broken_boundaries_of_fp16_gradients():
+    """Boundaries past the tensors, decreasing or negative, and maxima that are too small: told, and kept inside."""
+    j = Jagged([20, 30], [50, 90], 2, 2, 64, "f16")
+    O, L = j.forward()
+    good = j.backward(O, L)
+    _ok()
+    for q_off, kv_off in (([0, 20, 99], [0, 50, 140]), ([0, 20, 50], [0, 50, 200]), ([0, 20, 50], [0, 50, 10]),
+                          ([-7, 20, 50], [0, 50, 140]), ([0, 20, 50], [2000000000, -5, 140])):
+        j.q_off, j.kv_off = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (q_off, kv_off))
+        j.backward(O, L)
+        assert _status() == wk.WK_ERR_DEVICE
+    j.q_off, j.kv_off = U.offsets([20, 30]), U.offsets([50, 90])
+    for most in ((29, 90), (30, 89), (0, 90), (30, 0)):
+        j.max_q, j.max_kv = most
+        j.backward(O, L)
+        assert _status() == wk.WK_ERR_DEVICE
+    j.max_q, j.max_kv = 30, 90
+    again = j.backward(O, L)
+    _ok()
+    for a, b in zip(good, again):
+        assert torch.equal(a[:50], b[:50])
