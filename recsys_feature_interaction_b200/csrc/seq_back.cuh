@@ -79,8 +79,8 @@ struct SbCfg {
 // bits down to 2^-26 of the bound. (Times `scale` alone, with dO of 2^-10 over 2048 keys, dQ was off by
 // 2 %; with dO V^T beyond 65504 it was infinite.) The norms come from a pass over V and dO before the
 // two kernels: the largest of each chunk of 32 tokens, so that a unit reads few, and each dO row's own,
-// because the rows' losses differ. It makes a training step at the 2-layer shape 140 us in fp16, so 128;
-// bf16 does without.
+// because the rows' losses differ. A training step at the 2-layer shape takes 140 us in fp16 with it and
+// 128 without; bf16 does without.
 constexpr int SEQ_CHUNK = 32;
 struct SeqRange {
   float* rows;  // [total_q, q_heads] squared norms of dO
@@ -114,7 +114,7 @@ __device__ __forceinline__ float seq_exp2i(int k) { return __uint_as_float(stati
 
 // The warps of blocks (b, V or dO, z) take the (chunk, key head) of sequence b in turn, four lanes to a
 // row and 16 rows' loads at a time; bound by the latency of offsets, rows and the reduction, one after
-// the other (33 MB of V at the 2-layer shape: 12.4 us of cold inputs; 14.3 with chunks of 128 and a block
+// the other (33 MB of V at the 2-layer shape: 12.4 us from cold caches; 14.3 with chunks of 128 and a block
 // each, 14.1 with two chunks to a warp and 32 rows at a time).
 template <int D, typename T>
 __global__ void __launch_bounds__(256)
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
     float* cols = red + (warp - 4) * 128;  // DKV: lse (base 2) [32] and delta [32] of this warp's columns, twice
     uint32_t g = 0, uc = 0;
     bool ok = true;
-    int high_at = -1;  // fp16: the (sequence, key head) whose largest norms `high` holds
+    int64_t high_at = -1;  // fp16: the (sequence, key head) whose largest norms `high` holds
     float high = 0.f;
     SeqUnit u;
     for (;;) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(SbCfg<D, DKV>::THREADS, 1)
         float ds_in = a.scale, ds_out = 1.f;
         float lse2 = 0.f, dl = 0.f;
         if constexpr (!Half16<T>::kBF16) {
-          const int at = u.b * a.kv_heads + u.h;
+          const int64_t at = static_cast<int64_t>(u.b) * a.kv_heads + u.h;
           if (at != high_at) {
             high_at = at;
             high = seq_chunks_max(range.v, u.kv_begin, u.b, u.len, a.kv_heads, u.h);

@@ -703,14 +703,15 @@ __global__ void __launch_bounds__(StCfg<D, SRC>::THREADS, 1)
                 pk[2 * c4] = Half16<T>::pack2(seq_ex2(s[0] + (x.x + nw)), seq_ex2(s[1] + (x.y + nw)));
                 pk[2 * c4 + 1] = Half16<T>::pack2(seq_ex2(s[2] + (x.z + nw)), seq_ex2(s[3] + (x.w + nw)));
               }
-            } else
+            } else {
 #pragma unroll
-            for (int c2 = 0; c2 < KB / 4; ++c2) {
-              const float2 x =
-                  seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
-              const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(seq_ex2(x.x), seq_ex2(x.y));
-              sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
-              pk[c2] = Half16<T>::pack2(p.x, p.y);
+              for (int c2 = 0; c2 < KB / 4; ++c2) {
+                const float2 x =
+                    seq_fma2(make_float2(__uint_as_float(sr[2 * c2]), __uint_as_float(sr[2 * c2 + 1])), sc, nm2);
+                const float2 p = c2 % 4 == 3 ? seq_ex2_poly(x) : make_float2(seq_ex2(x.x), seq_ex2(x.y));
+                sum[c2 & 1] = seq_add2(sum[c2 & 1], p);
+                pk[c2] = Half16<T>::pack2(p.x, p.y);
+              }
             }
             if (warp_on) whale_tmem_st32(ta + at / 2, pk);
             whale_tmem_st_wait();
